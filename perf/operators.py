@@ -78,15 +78,10 @@ def draw(rng):
 # ---- inputs ---------------------------------------------------------------------------------
 
 
-def _over(t, c):
-    """t / c rounded as IEEE does (the library multiplies by a rounded 1 / c where c is a plain number)."""
-    return t / torch.full_like(t, c)
-
-
 def _q8(y):
     """Rows of y (fp32) in 8 bits: e4m3 codes and the scale of each row."""
     amax = y.abs().amax(dim=1, keepdim=True)
-    scale = _over(amax, Q8_MAX)
+    scale = amax / Q8_MAX
     q = torch.where(amax > 0, y / scale, torch.zeros_like(y))
     return q.to(torch.float8_e4m3fn), scale[:, 0]
 
@@ -97,9 +92,9 @@ def _w4(w, G, zeros):
     g = w.float().view(N, K // G, G)
     if zeros:
         lo, hi = g.amin(dim=2).clamp(max=0.0), g.amax(dim=2).clamp(min=0.0)
-        scale = _over(hi - lo, 15.0).to(torch.bfloat16)
+        scale = ((hi - lo) / 15.0).to(torch.bfloat16)
     else:
-        scale = _over(g.abs().amax(dim=2), 7.0).to(torch.bfloat16)
+        scale = (g.abs().amax(dim=2) / 7.0).to(torch.bfloat16)
     s = scale.float()
     one = torch.where(s > 0, s, torch.ones_like(s))
     zp = torch.round(-lo / one).clamp(0, 15) if zeros else torch.full_like(s, 8.0)
@@ -249,9 +244,8 @@ def work(case):
 
 def _nearest_e4m3(v):
     """v (float64) rounded to the nearest e4m3 value, ties to even, saturating at 448."""
-    part, _ = torch.frexp(v)  # v = part 2^e with |part| in [0.5, 1)
-    power = torch.where(v != 0, v / (2 * part), torch.ones_like(v))  # 2^(e-1), an exact quotient
-    step = power.clamp(min=2.0 ** -6) / 8
+    _, e = torch.frexp(v)  # |v| in [2^(e-1), 2^e)
+    step = torch.ldexp(torch.ones_like(v), (e - 1).clamp(min=-6) - 3)
     return (torch.round(v / step) * step).clamp(-Q8_MAX, Q8_MAX)
 
 
