@@ -504,7 +504,16 @@ int qwen3_sample(const float *logits_dev, int32_t B, int32_t V, const float *tem
  * writes memory only once the work before it in its stream is done, and lets the next kernel launch
  * meanwhile: one of the caller's own that is launched with the programmatic attribute right after it
  * has to wait (griddepcontrol.wait) likewise.  An output must not overlap an input other than where a
- * call says so. */
+ * call says so.
+ *
+ * Every wait of these kernels on a copy or on the tensor cores is bounded (qwen3_op_set_wait_limit).  A wait
+ * that gives up leaves NaN in the outputs that depended on it -- never old or unwritten ones -- once the
+ * kernel's own copies have landed; the calls return before they run, so this is how it shows. */
+
+/* Sets the limit, in SM clock cycles, of the waits of the calls on 8-bit and 4-bit operands made after this
+ * one, in the whole process (a captured graph keeps the limit that it was captured with); 0, the default, is
+ * 2^31 cycles (about a second).  A limit of a cycle or so makes the waits give up on purpose, to test for it. */
+void qwen3_op_set_wait_limit(uint32_t cycles);
 
 #define QWEN3_DT_F32 0
 #define QWEN3_DT_BF16 1

@@ -130,6 +130,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "qwen3_op_attn_decode_plan": (i32, [i32, i32, i32, i32, i32]),
         "qwen3_op_attn_decode": (ctypes.c_int, [_P, i32, _P, pi32, _P, pi32, _P, _P, _P, _P, _P, i32, i32, i32, i32,
                                                 ctypes.c_float, i32, _P, _P, sz, _P]),
+        "qwen3_op_set_wait_limit": (None, [ctypes.c_uint32]),
         "qwen3_op_quant_q8": (ctypes.c_int, [_P, i32, i32, i32, _P, _P, _P]),
         "qwen3_op_add_rmsnorm_q8": (ctypes.c_int, [_P, _P, i32, i32, i32, _P, ctypes.c_float, _P, _P, _P]),
         "qwen3_op_gemm_q8": (ctypes.c_int, [_P, _P, i32, i32, _P, _P, i32, i32, _P, _P]),
@@ -407,6 +408,14 @@ def sample(logits, temperature, top_k, top_p, uniform, out=None):
 
 
 # --- 8-bit and 4-bit operands ---------------------------------------------------------------
+
+def qwen3_op_set_wait_limit(cycles: int):
+    """Limit of the waits of the calls below, in SM clock cycles; 0 restores the default.  A wait that
+    gives up leaves NaN in the outputs."""
+    if not 0 <= cycles < 2 ** 32:
+        raise Qwen3Error(QWEN3_E_INVALID, "qwen3_op_set_wait_limit: cycles outside [0, 2^32)")
+    load_library().qwen3_op_set_wait_limit(cycles)
+
 
 def qwen3_op_quant_q8(x_ptr: int, x_dtype: int, M: int, K: int, q_ptr: int, scale_ptr: int, stream: int = 0):
     _check(load_library().qwen3_op_quant_q8(x_ptr, x_dtype, M, K, q_ptr, scale_ptr, stream), None)

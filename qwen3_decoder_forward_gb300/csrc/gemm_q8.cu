@@ -27,7 +27,9 @@
 // in distributed shared memory in a fixed order.  33 x 1024 x 2048 with the residual: 3.9 us.
 // M, N and K need not fill tiles: TMA zero-fills past the tensors' ends (a zero code adds
 // nothing) and drops what is stored past them; N and K are multiples of 16.
-// Every mbarrier wait is bounded.
+// Every mbarrier wait is bounded.  A role that gives up stops; the epilogue then gives up too, and what it had not
+// finished is NaN in the outputs.  No CTA leaves, or reuses its ring, before the copies it issued have landed and the
+// MMAs have completed.
 
 #include "kernels.h"
 #include "tc.cuh"
@@ -63,10 +65,7 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p != 0;
 }
-// A bounded wait of a whole warp, with one answer for all of it.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t phase) {
-    return __all_sync(0xffffffffu, mbar_try_wait(bar, phase) || mbar_wait_bounded(bar, phase, nullptr));
-}
+constexpr uint32_t NAN_BITS = 0x7fffffffu;
 // Place in a ring of N stages and the parity of the round there.
 template <int N>
 struct Ring {
@@ -178,6 +177,22 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t *v) {
         : "memory");
 }
 
+// What an epilogue warp's wait that gave up leaves: NaN in row r and the warp's columns of tile t and of the CTA's tiles
+// after it.  A call, so that its code is not in the way of ordinary launches.
+template <int BN, int EPI>
+__device__ __noinline__ void store_nan(long long t, long long tiles, long long step, int tiles_n, int r, int half, int M, int N,
+                                       void *out) {
+    for (; t < tiles; t += step) {
+        const int row = (int)(t / tiles_n) * G8_BM + r, n0 = (int)(t % tiles_n) * BN;
+        for (int c = half; c < BN / 16; c += 2)
+            for (int col = n0 + c * 16; row < M && col < min(N, n0 + c * 16 + 16); ++col)
+                if (EPI != EPI_SWIGLU)
+                    static_cast<float *>(out)[(size_t)row * N + col] = __uint_as_float(NAN_BITS);
+                else if (col % 2 == 0)
+                    static_cast<uint16_t *>(out)[(size_t)row * (N / 2) + col / 2] = 0x7fff;
+    }
+}
+
 // Rows of x in a box: 128, or all there are in whole swizzle groups (16 rows of x against
 // 4096 x 4096 weights: 14.4 us with boxes of 128 rows, mostly zero fill, 10.8 with 16).
 __host__ __device__ constexpr uint32_t q8_box_rows(int M) { return M >= 128 ? 128 : (M + 7) / 8 * 8; }
@@ -186,7 +201,7 @@ template <int BN, int EPI, bool SPLIT>
 __global__ void __launch_bounds__(G8_THREADS, 1) k_gemm_q8(const __grid_constant__ CUtensorMap tmA,
                                                            const __grid_constant__ CUtensorMap tmB,
                                                            const float *__restrict__ xs, const float *__restrict__ ws, int M,
-                                                           int N, int K, void *out, int S) {
+                                                           int N, int K, void *out, int S, long long limit) {
     using T = G8<BN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -194,7 +209,9 @@ __global__ void __launch_bounds__(G8_THREADS, 1) k_gemm_q8(const __grid_constant
     uint64_t *empty = full + T::STAGES;
     uint64_t *tm_full = empty + T::STAGES;  // [2]
     uint64_t *tm_empty = tm_full + 2;       // [2]
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tm_empty + 2);
+    uint64_t *drained = tm_empty + 2;       // the MMAs issued, where a wait gave up
+    uint64_t *idle = drained + 1;           // no copy and no MMA is in flight
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(idle + 1);
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     // this CTA's k-blocks: all, or its share of the cluster's tile
@@ -216,6 +233,8 @@ __global__ void __launch_bounds__(G8_THREADS, 1) k_gemm_q8(const __grid_constant
             mbar_init(&tm_full[a], 1);
             mbar_init(&tm_empty[a], G8_EPI_WARPS);  // one arrival per epilogue warp
         }
+        mbar_init(drained, 1);
+        mbar_init(idle, 2);  // the warps that issue
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
@@ -237,7 +256,7 @@ __global__ void __launch_bounds__(G8_THREADS, 1) k_gemm_q8(const __grid_constant
         for (long long t = first; t < tiles && ok; t += step) {
             const int m0 = (int)(t / tiles_n) * G8_BM, n0 = (int)(t % tiles_n) * BN;
             for (int kb = 0; kb < KB; ++kb, ++it, r.next()) {
-                if (it >= T::STAGES && !warp_wait(&empty[r.s], r.round ^ 1)) {
+                if (it >= T::STAGES && !warp_wait(&empty[r.s], r.round ^ 1, limit)) {
                     ok = false;
                     break;
                 }
@@ -249,9 +268,11 @@ __global__ void __launch_bounds__(G8_THREADS, 1) k_gemm_q8(const __grid_constant
                 }
             }
         }
-        if (!ok)  // let the copies in flight land before the CTA can leave
-            for (uint32_t j = (it > T::STAGES ? it - T::STAGES : 0); j < it; ++j)
-                mbar_wait_bounded(&full[j % T::STAGES], (j / T::STAGES) & 1, nullptr);
+        // the ring's last copies land before the CTA can leave, whether or not their MMAs are issued
+#pragma unroll 1
+        for (uint32_t s = 0; s < (it < T::STAGES ? it : T::STAGES); ++s)
+            warp_wait(&full[s], s < r.s ? r.round : r.round ^ 1, WAIT_LIMIT_DEFAULT);
+        if (SPLIT && issues) mbar_arrive_cta(idle);
     } else if (warp == 1) {
         constexpr uint32_t idesc = idesc_e4m3(G8_BM, BN);
         const bool issues = elect_one();
@@ -260,11 +281,14 @@ __global__ void __launch_bounds__(G8_THREADS, 1) k_gemm_q8(const __grid_constant
         bool ok = true;
         for (long long t = first; t < tiles && ok; t += step, ++local) {
             const uint32_t a = local & 1;
-            if (local >= 2 && !warp_wait(&tm_empty[a], ((local >> 1) & 1) ^ 1)) break;
+            if (local >= 2 && !warp_wait(&tm_empty[a], ((local >> 1) & 1) ^ 1, limit)) {
+                ok = false;
+                break;
+            }
             tc_fence_after();
             const uint32_t acc = tmem + a * BN;
             for (int kb = 0; kb < KB; ++kb, r.next()) {
-                if (!warp_wait(&full[r.s], r.round)) {
+                if (!warp_wait(&full[r.s], r.round, limit)) {
                     ok = false;
                     break;
                 }
@@ -278,6 +302,10 @@ __global__ void __launch_bounds__(G8_THREADS, 1) k_gemm_q8(const __grid_constant
             if (ok && issues) tc_commit(&tm_full[a]);
         }
         __syncwarp();
+        // the MMAs complete before the CTA can leave, whether or not the epilogue waits for them
+        if (!ok && issues) tc_commit(drained);
+        warp_wait(ok ? &tm_full[(local - 1) & 1] : drained, ok ? ((local - 1) >> 1) & 1 : 0, WAIT_LIMIT_DEFAULT);
+        if (SPLIT && issues) mbar_arrive_cta(idle);
     } else {
         const int q = warp & 3;            // TMEM lane quarter this warp may access
         const int half = (warp - 2) >> 2;  // 16-column chunks half, half + 2, ... of the tile
@@ -289,7 +317,8 @@ __global__ void __launch_bounds__(G8_THREADS, 1) k_gemm_q8(const __grid_constant
             const bool live = row < M;
             const float sx = live ? xs[row] : 0.0f;
             if (SPLIT) {  // its sums into shared memory, over the ring that the MMAs are done with
-                const bool done = __all_sync(0xffffffffu, mbar_wait_bounded(&tm_full[a], 0, nullptr));
+                const bool done = warp_poll(&tm_full[a], 0, limit);
+                if (!done) warp_wait(idle, 0, WAIT_LIMIT_DEFAULT);
                 tc_fence_after();
                 float4 *dst = reinterpret_cast<float4 *>(smem + (q * 32 + lane) * T::PITCH);
 #pragma unroll
@@ -298,7 +327,7 @@ __global__ void __launch_bounds__(G8_THREADS, 1) k_gemm_q8(const __grid_constant
                     tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + c * 16, v);
                     if (!done)  // a wait gave up: the outputs say so
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] = 0x7fffffffu;
+                        for (int j = 0; j < 16; ++j) v[j] = NAN_BITS;
                     if (live)
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
@@ -309,7 +338,10 @@ __global__ void __launch_bounds__(G8_THREADS, 1) k_gemm_q8(const __grid_constant
             }
             Out16<EPI> o;
             if (n0 + half * 16 < N) o.read(ws, out, row, n0 + half * 16, N, live);
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tm_full[a], (local >> 1) & 1, nullptr))) break;
+            if (!warp_poll(&tm_full[a], (local >> 1) & 1, limit)) {  // NaN in this tile and in those after it
+                store_nan<BN, EPI>(t, tiles, step, tiles_n, q * 32 + lane, half, M, N, out);
+                break;
+            }
             tc_fence_after();
             const uint32_t t_row = tmem + a * BN + ((uint32_t)(q * 32) << 16);
 #pragma unroll 1
@@ -384,10 +416,10 @@ __global__ void __launch_bounds__(G8_THREADS, 1) k_gemm_q8(const __grid_constant
                 }
             }
         }
-            __syncwarp();
+        __syncwarp();
         cluster_sync();  // no CTA leaves while another reads its shares
     } else {
-            __syncthreads();
+        __syncthreads();
     }
     if (warp == 1) {
         tc_fence_after();
@@ -443,6 +475,14 @@ __device__ __forceinline__ void commit_pair(uint64_t *bar) {
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// A word of either CTA's shared memory.
+__device__ __forceinline__ void store_to(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// Takes `bytes` that will not come off what a barrier of this CTA expects.
+__device__ __forceinline__ void complete_tx(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
+}
 // A shared tile to the output: stored, or added to it.  The caller commits the group.
 template <bool ADD>
 __device__ __forceinline__ void tile_out(const CUtensorMap *map, const void *src, int x, int y) {
@@ -476,14 +516,17 @@ template <int EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
     k_gemm_q8_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmO, const float *__restrict__ xs, const float *__restrict__ ws,
-                   int M, int N, int K) {
+                   int M, int N, int K, long long limit) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + P8_BARS);  // [stages], those of CTA 0 in use
     uint64_t *empty = full + P8_STAGES;                             // [stages]
     uint64_t *tm_full = empty + P8_STAGES;                          // [2]
     uint64_t *tm_empty = tm_full + 2;                               // [2], those of CTA 0 in use
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tm_empty + 2);
+    uint64_t *drained = tm_empty + 2;                               // all MMAs, at the end
+    uint64_t *met = drained + 1;                                    // CTA 1 has issued its last load; CTA 0's in use
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(met + 1);
+    uint32_t *issued1 = tmem_slot + 1;  // k-blocks that CTA 1 issued, then
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cta_rank();
@@ -501,6 +544,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
             mbar_init(&tm_full[a], 1);
             mbar_init(&tm_empty[a], 2 * P8_EPI_WARPS);  // one arrival per epilogue warp of the pair
         }
+        mbar_init(drained, 1);
+        mbar_init(met, 1);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(tmem_slot)));
@@ -523,7 +568,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
             const int m0 = (int)(t / tiles_n) * P8_BM + (int)rank * 128;
             const int n0 = (int)(t % tiles_n) * P8_BN + (int)rank * 128;
             for (int kb = 0; kb < KB; ++kb, ++it, r.next()) {
-                if (it >= P8_STAGES && !warp_wait(&empty[r.s], r.round ^ 1)) {
+                if (it >= P8_STAGES && !warp_wait(&empty[r.s], r.round ^ 1, limit)) {
                     ok = false;
                     break;
                 }
@@ -536,10 +581,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
                 }
             }
         }
-        // The ring's last loads land before the CTA can leave: CTA 0 waits for both CTAs' bytes.
-        if (rank == 0)
-            for (uint32_t j = (it > P8_STAGES ? it - P8_STAGES : 0); j < it; ++j)
-                if (!warp_wait(&full[j % P8_STAGES], (j / P8_STAGES) & 1)) break;
+        // The ring's last loads land before a CTA can leave, whether or not their MMAs are issued: CTA 0 waits for both
+        // CTAs' bytes.  Where a wait gave up, one may have issued up to a ring more k-blocks than the other, and
+        // CTA 0 makes its barriers whole first.
+        if (rank == 1) {
+            if (issues) {
+                store_to(in_cta(issued1, 0), it);
+                asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_cta(met, 0)) : "memory");
+            }
+        } else {
+            const bool here = warp_wait(met, 0, WAIT_LIMIT_DEFAULT);
+            asm volatile("fence.acq_rel.cluster;" ::: "memory");
+            const uint32_t other = here ? *static_cast<volatile uint32_t *>(issued1) : it, most = it > other ? it : other;
+            if (it != other && issues)
+                for (uint32_t j = it < other ? it : other; j < most; ++j) {
+                    if (it < other)
+                        mbar_expect_tx(&full[j % P8_STAGES], P8_STAGE);  // CTA 1's bytes alone
+                    else
+                        complete_tx(&full[j % P8_STAGES], P8_STAGE);  // CTA 1's will not come
+                }
+            __syncwarp();
+            for (uint32_t j = (most > P8_STAGES ? most - P8_STAGES : 0); j < most; ++j)
+                warp_wait(&full[j % P8_STAGES], (j / P8_STAGES) & 1, WAIT_LIMIT_DEFAULT);
+        }
     } else if (warp == 1) {
         if (rank == 0) {
             constexpr uint32_t idesc = idesc_e4m3(P8_BM, P8_BN);
@@ -549,11 +613,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
             bool ok = true;
             for (long long t = first; t < tiles && ok; t += step, ++local) {
                 const uint32_t a = local & 1;
-                if (local >= 2 && !warp_wait(&tm_empty[a], ((local >> 1) & 1) ^ 1)) break;
+                if (local >= 2 && !warp_wait(&tm_empty[a], ((local >> 1) & 1) ^ 1, limit)) break;
                 tc_fence_after();
                 const uint32_t acc = tmem + a * P8_BN;
                 for (int kb = 0; kb < KB; ++kb, r.next()) {
-                    if (!warp_wait(&full[r.s], r.round)) {
+                    if (!warp_wait(&full[r.s], r.round, limit)) {
                         ok = false;
                         break;
                     }
@@ -566,17 +630,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
                 }
                 if (ok && issues) commit_pair(&tm_full[a]);
             }
+            if (issues) commit_pair(drained);
             __syncwarp();
+        }
+        // the MMAs complete, and their arrivals are here, before a CTA can leave, whether or not its epilogue waited
+        for (long long t = first; t < tiles && !warp_wait(drained, 0, WAIT_LIMIT_DEFAULT); t += step) {
         }
     } else {
         const int q = warp & 3;            // TMEM lane quarter this warp may access
         const int part = (warp - 2) >> 2;  // 64 columns of the tile
         uint8_t *buf = smem + P8_OUT + (warp - 2) * P8_TILE;
         uint32_t local = 0;
+        bool gave_up = false;
         for (long long t = first; t < tiles; t += step, ++local) {
             const uint32_t a = local & 1;
             const int y = (int)(t / tiles_n) * P8_BM + (int)rank * 128 + q * 32, n0 = (int)(t % tiles_n) * P8_BN + part * 64;
-            const float sx = y + lane < M ? __ldg(xs + y + lane) : 0.0f;
+            float sx = y + lane < M ? __ldg(xs + y + lane) : 0.0f;
             // 16 columns' scales, the first ones while the MMAs run; columns past N, a multiple of 16,
             // take others' and are not stored
             float4 w[4];
@@ -586,7 +655,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
                 for (int j = 0; j < 4; ++j) w[j] = __ldg(p + j);
             };
             read_scales(n0);
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tm_full[a], (local >> 1) & 1, nullptr))) break;
+            // a wait that gave up leaves NaN in this tile and in those after it (added to a residual, too)
+            gave_up = gave_up || !warp_poll(&tm_full[a], (local >> 1) & 1, limit);
+            if (gave_up) sx = __uint_as_float(NAN_BITS);
             tc_fence_after();
             const uint32_t t_row = tmem + a * P8_BN + part * 64 + ((uint32_t)(q * 32) << 16);
             // the tile's rows of 64 bytes: 16-byte piece u of row r at u ^ (r / 2) % 4 (64-byte swizzle)
@@ -610,7 +681,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
                 if (c == 3) {  // the accumulator has been read
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) arrive_at(in_cta(&tm_empty[a], 0));
+                    if (lane == 0 && !gave_up) arrive_at(in_cta(&tm_empty[a], 0));
                 }
                 float2 v[8];
 #pragma unroll
@@ -675,7 +746,8 @@ cudaError_t run_pair(const Launch &lc, const uint8_t *xq, const float *xs, int M
     if (e != cudaSuccess) return e;
     const long long tiles = (long long)((M + P8_BM - 1) / P8_BM) * ((N + P8_BN - 1) / P8_BN);
     const int pairs = (int)(tiles < lc.num_sms / 2 ? tiles : lc.num_sms / 2);
-    return launch(lc, k_gemm_q8_pair<EPI>, dim3(2 * pairs), dim3(P8_THREADS), P8_SMEM, ma, mb, mo, xs, ws, M, N, K);
+    return launch(lc, k_gemm_q8_pair<EPI>, dim3(2 * pairs), dim3(P8_THREADS), P8_SMEM, ma, mb, mo, xs, ws, M, N, K,
+                  lc.wait_limit);
 }
 
 template <int BN, int EPI, bool SPLIT>
@@ -689,9 +761,10 @@ cudaError_t run_q8(const Launch &lc, const uint8_t *xq, const float *xs, int M, 
     const long long tiles = (long long)((M + G8_BM - 1) / G8_BM) * ((N + BN - 1) / BN);
     if (SPLIT)
         return launch_cluster(lc, k_gemm_q8<BN, EPI, SPLIT>, dim3((unsigned)(tiles * S)), dim3(G8_THREADS), G8<BN>::SMEM,
-                              dim3(S, 1, 1), ma, mb, xs, ws, M, N, K, out, S);
+                              dim3(S, 1, 1), ma, mb, xs, ws, M, N, K, out, S, lc.wait_limit);
     const int grid = (int)(tiles < lc.num_sms ? tiles : lc.num_sms);
-    return launch(lc, k_gemm_q8<BN, EPI, SPLIT>, dim3(grid), dim3(G8_THREADS), G8<BN>::SMEM, ma, mb, xs, ws, M, N, K, out, 1);
+    return launch(lc, k_gemm_q8<BN, EPI, SPLIT>, dim3(grid), dim3(G8_THREADS), G8<BN>::SMEM, ma, mb, xs, ws, M, N, K, out, 1,
+                  lc.wait_limit);
 }
 template <int BN, int EPI>
 cudaError_t run_single(const Launch &lc, const uint8_t *xq, const float *xs, int M, int K, const uint8_t *wq, const float *ws,

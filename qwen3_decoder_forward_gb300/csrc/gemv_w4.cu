@@ -48,6 +48,7 @@ struct W4Args {
     int S;         // CTAs of a cluster sharing the columns
     int kslice;    // columns of a CTA of the cluster, a multiple of 256
     int xstride;   // bytes of a staged row of x, 64 modulo 128
+    long long limit;  // of a wait, in clocks
 };
 
 // MT: 8-row tiles of x.
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(W4<ZEROS, G, MT>::MAX_WARPS * 32, 1)
         for (int j = 0; j < mine && ok; ++j, ++u) {
             const int s = u % W4_ST;
             const uint32_t phase = (u / W4_ST) & 1;
-            if (!__all_sync(0xffffffffu, mbar_try_wait(&full[s], phase) || mbar_wait_bounded(&full[s], phase, nullptr))) {
+            if (!warp_poll(&full[s], phase, a.limit)) {
                 ok = false;
                 break;
             }
@@ -618,6 +619,7 @@ cudaError_t launch_gemv_w4(const Launch &lc, const void *x, const float *xs, int
         a.zeros = zeros;
         a.out = static_cast<uint8_t *>(out) + (size_t)m0 * N * (epi == EPI_SWIGLU ? 1 : 4);
         a.epi = epi;
+        a.limit = lc.wait_limit;
         const cudaError_t e = xs ? (zeros ? run_group<true, true>(lc, a, codes, group) : run_group<true, false>(lc, a, codes, group))
                                  : (zeros ? run_group<false, true>(lc, a, codes, group) : run_group<false, false>(lc, a, codes, group));
         if (e != cudaSuccess) return e;

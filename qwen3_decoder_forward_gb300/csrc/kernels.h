@@ -19,6 +19,7 @@ struct Launch {
     bool pdl = true;          // programmatic dependent launch on every kernel
     int num_sms = 148;
     int64_t *counter = nullptr;
+    long long wait_limit = WAIT_LIMIT_DEFAULT;  // the kernels on 8-bit and 4-bit operands: clocks of a bounded wait
 };
 
 // Every kernel asks for the largest shared-memory carveout, so that the L1/shared split is the

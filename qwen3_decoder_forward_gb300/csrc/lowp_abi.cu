@@ -1,6 +1,7 @@
 // C ABI of the single kernels on 8-bit and 4-bit operands: argument checks and launches.  See
 // include/qwen3_gb300.h for the contract of every call.
 
+#include <atomic>
 #include <cmath>
 #include <string>
 
@@ -35,8 +36,11 @@ bool dtype_ok(int32_t t) { return t == QWEN3_DT_F32 || t == QWEN3_DT_BF16; }
 
 constexpr int32_t MAX_SIZE = 1 << 30;  // rows or columns: sums with a tile stay in 32 bits
 
+std::atomic<uint32_t> wait_limit_cycles{0};  // 0: the default
+
 cudaError_t make_launch(void *stream, Launch *lc) {
     lc->stream = static_cast<cudaStream_t>(stream);
+    if (const uint32_t cycles = wait_limit_cycles.load(std::memory_order_relaxed)) lc->wait_limit = cycles;
     // Every kernel here touches memory only after the one before it in the stream is done, and then lets
     // the next one launch, whose start hides behind it (back to back from Python: 13 rows of 8192 x
     // 10240 25.8 -> 23.4 us then, 23,460 rows quantised 28.9 -> 25.6; in a graph one row of q/k/v 3.9 -> 3.3).
@@ -61,6 +65,8 @@ int guarded(F body) noexcept {
 }  // namespace
 
 extern "C" {
+
+void qwen3_op_set_wait_limit(uint32_t cycles) { wait_limit_cycles.store(cycles, std::memory_order_relaxed); }
 
 int qwen3_op_quant_q8(const void *x, int32_t x_dtype, int32_t M, int32_t K, void *q, float *scale, void *stream) {
     return guarded([&]() -> int {

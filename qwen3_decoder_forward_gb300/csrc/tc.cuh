@@ -63,6 +63,29 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *v) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// Waits of a whole warp for phase `phase` of `bar`, for at most `limit` SM cycles, with one answer for all of it.
+// warp_poll does not suspend under a limit other than the default, as mbar_wait_ctx does, so that one of a few cycles
+// makes it give up; warp_wait always does (in loops that issue MMAs the choice cost 0.1 us of 11).
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t phase, long long limit) {
+    bool ok = mbar_try_wait(bar, phase);
+    if (!ok) {
+        const long long t0 = clock64();
+        while (!(ok = mbar_try_wait(bar, phase)))
+            if (clock64() - t0 > limit) break;
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ bool warp_poll(uint64_t *bar, uint32_t phase, long long limit) {
+    bool ok = mbar_test_wait(bar, phase);
+    if (!ok) {
+        const bool usual = limit == WAIT_LIMIT_DEFAULT;
+        const long long t0 = clock64();
+        while (!(ok = usual ? mbar_try_wait(bar, phase) : mbar_test_wait(bar, phase)))
+            if (clock64() - t0 > limit) break;
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
