@@ -75,6 +75,14 @@ __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.lau
 
 __device__ __forceinline__ float silu(float x) { return x / (1.0f + __expf(-x)); }
 
+// silu(g) u for any g: with e = exp(-|g|) <= 1 nothing overflows where silu is not zero (exp(-g) does from -88.7 on, and
+// __fdividef by more than 2^126 is zero).  The fast exponential and division are a few ulp off, some 100 at
+// |g| = 88: far below the bf16 rounding that follows.
+__device__ __forceinline__ float swiglu(float g, float u) {
+    const float e = __expf(-fabsf(g));
+    return __fdividef(g < 0.0f ? g * e : g, 1.0f + e) * u;
+}
+
 // ---- mbarrier + bulk asynchronous copies (TMA engine, untiled) ---------------------------
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {

@@ -148,7 +148,7 @@ struct Out16 {
             uint32_t o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                o[j] = pack_bf16x2(silu(y[4 * j]) * y[4 * j + 1], silu(y[4 * j + 2]) * y[4 * j + 3]);
+                o[j] = pack_bf16x2(swiglu(y[4 * j], y[4 * j + 1]), swiglu(y[4 * j + 2], y[4 * j + 3]));
             *reinterpret_cast<uint4 *>(static_cast<bf16 *>(out) + row * (N / 2) + col / 2) = make_uint4(o[0], o[1], o[2], o[3]);
         } else {
             float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(out) + row * N + col);
@@ -399,8 +399,8 @@ __global__ void __launch_bounds__(G8_THREADS, 1) k_gemm_q8(const __grid_constant
                 }
                 if (EPI == EPI_SWIGLU) {
                     uint2 o;
-                    o.x = pack_bf16x2(silu(y[0]) * y[1], silu(y[2]) * y[3]);
-                    o.y = pack_bf16x2(silu(y[W - 4]) * y[W - 3], silu(y[W - 2]) * y[W - 1]);
+                    o.x = pack_bf16x2(swiglu(y[0], y[1]), swiglu(y[2], y[3]));
+                    o.y = pack_bf16x2(swiglu(y[W - 4], y[W - 3]), swiglu(y[W - 2], y[W - 1]));
                     *reinterpret_cast<uint2 *>(static_cast<bf16 *>(out) + (size_t)(m0 + r) * (N / 2) + col / 2) = o;
                 } else {
                     float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(out) + (size_t)(m0 + r) * N + col);
@@ -507,10 +507,6 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(z));
     return r;
 }
-
-// silu(gu.x) * gu.y with the fast exponential and division: a few ulp, far below the bf16 rounding
-// after it.
-__device__ __forceinline__ float swiglu_fast(float2 gu) { return __fdividef(gu.x, 1.0f + __expf(-gu.x)) * gu.y; }
 
 template <int EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
@@ -696,7 +692,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
                 if (EPI == EPI_SWIGLU) {  // 16 columns are one piece of the tile's rows
                     uint32_t o[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) o[j] = pack_bf16x2(swiglu_fast(v[2 * j]), swiglu_fast(v[2 * j + 1]));
+                    for (int j = 0; j < 4; ++j) o[j] = pack_bf16x2(swiglu(v[2 * j].x, v[2 * j].y), swiglu(v[2 * j + 1].x, v[2 * j + 1].y));
                     if (c == 0) buffer_free();
                     *reinterpret_cast<uint4 *>(out_row + ((c ^ sw) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                     if (c == 3) store_tile(n0 / 2, y < M && n0 < N);

@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(W4<ZEROS, G, MT>::MAX_WARPS * 32, 1)
                         for (int r = 0; r < RM * 2; ++r) {
                             const float up = __shfl_xor_sync(0xffffffffu, v[r], 4);
                             if (!(g & 1) && m < a.M && n0 + r * 8 < a.N)
-                                static_cast<bf16 *>(a.out)[(size_t)m * (a.N / 2) + (n0 + r * 8) / 2] = __float2bfloat16(silu(v[r]) * up);
+                                static_cast<bf16 *>(a.out)[(size_t)m * (a.N / 2) + (n0 + r * 8) / 2] = __float2bfloat16(swiglu(v[r], up));
                         }
                     } else {
                         float *o = static_cast<float *>(a.out);
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(W4<ZEROS, G, MT>::MAX_WARPS * 32, 1)
             const float sx = XQ ? xsc[m] : 1.0f;
             if (a.epi == EPI_SWIGLU) {
                 const float2 v = total(rank * rows + r, m, make_float2(0.0f, 0.0f));
-                static_cast<bf16 *>(a.out)[(size_t)m * (a.N / 2) + n / 2] = __float2bfloat16(silu(v.x * sx) * (v.y * sx));
+                static_cast<bf16 *>(a.out)[(size_t)m * (a.N / 2) + n / 2] = __float2bfloat16(swiglu(v.x * sx, v.y * sx));
             } else {
                 const float v = total(rank * rows + r, m, 0.0f) * sx;
                 float *o = static_cast<float *>(a.out) + (size_t)m * a.N + n;

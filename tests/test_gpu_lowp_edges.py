@@ -1,0 +1,74 @@
+"""Edges of the single kernels on 8-bit and 4-bit operands: values far from 1, against their
+definitions in 64 bits.
+
+Tolerances: a projection's sums as in test_gpu_lowp.py, (K / 16 + 8) 2^-23 of the terms' magnitudes; a
+rounding is half a step of its type.
+"""
+
+import pytest
+import torch
+
+import gpu_common as gc
+from qwen3_decoder_forward_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+
+F32, RESID, SWIGLU = binding.QWEN3_EPI_F32, binding.QWEN3_EPI_RESID_ADD, binding.QWEN3_EPI_SWIGLU
+E4M3 = torch.float8_e4m3fn
+BF16_HALF = torch.finfo(torch.bfloat16).eps / 2
+
+# GEMM sizes (M, N, K) that run as pairs of CTAs, as single CTAs, and with K shared by a cluster
+FORMS = [(4000, 3584, 128), (200, 512, 128), (40, 512, 2048)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    gc.ensure_library()
+
+
+def _gates():
+    """Gates over the range in which silu leaves fp32's normal numbers, and ordinary ones."""
+    return torch.cat([torch.linspace(-105, -80, 200, dtype=torch.float64), torch.linspace(-12, 100, 56, dtype=torch.float64)]).float()
+
+
+def _check_swiglu(out, gate, up):
+    """exp's error at |g| <= 105 is 126 ulp by CUDA's table (2 + 1.173 |g|), the division's and the products'
+    a few: 2^-16 in all; a value below the normal numbers has steps of 2^-133 in bf16."""
+    g, u = gate.double(), up.double()
+    ref = g * torch.sigmoid(g) * u
+    tol = (BF16_HALF + 2 ** -16) * ref.abs() + 2.0 ** -133
+    # e^g itself is a subnormal of fp32 below -87.3, with steps of 2^-149, and so is a product with it
+    tol = tol + 2.0 ** -149 * (g.abs() * u.abs() + u.abs() + 1)
+    err = (out.double().cpu() - ref).abs()
+    worst = int((err / tol).argmax())
+    assert bool((err <= tol).all()), f"gate {float(g.flatten()[worst % g.numel()])}: error / tolerance {float((err / tol).max()):.3g}"
+
+
+@pytest.mark.parametrize("M,N,K", FORMS)
+@pytest.mark.parametrize("up", [1.0, -3e4, 1e30])
+def test_gemm_q8_swiglu_over_the_range_of_gates(M, N, K, up):
+    """One product of ones a row, so that gate and up are the weights' scales."""
+    gates = _gates()
+    xq, wq = torch.zeros(M, K), torch.zeros(N, K)
+    xq[:, 1] = 1
+    wq[:, 1] = 1
+    gate = gates.repeat(N // 2 // gates.numel() + 1)[: N // 2]
+    ws = torch.stack([gate, torch.full_like(gate, up)], dim=1).flatten()
+    out = binding.gemm_q8(xq.to(E4M3).cuda(), torch.ones(M, device="cuda"), wq.to(E4M3).cuda(), ws.cuda(), epilogue=SWIGLU)
+    assert torch.equal(out, out[:1].expand_as(out))
+    _check_swiglu(out[0], gate, torch.full_like(gate, up))
+
+
+@pytest.mark.parametrize("N,K", [(512, 128), (512, 4096), (40000, 128)])
+@pytest.mark.parametrize("up", [1.0, 1e30])
+def test_gemv_w4_swiglu_over_the_range_of_gates(N, K, up):
+    """One weight of a row is its scale, the others zero: gate and up are bf16 scales."""
+    gate = _gates().bfloat16().repeat(N // 512 + 1)[: N // 2]
+    codes = torch.full((N, K // 2), 0x88, dtype=torch.uint8)
+    codes[:, 0] = 0x89
+    scales = torch.ones(N, K // 32, dtype=torch.bfloat16)
+    scales[:, 0] = torch.stack([gate, torch.full_like(gate, up)], dim=1).flatten()
+    x = torch.ones(3, K, dtype=torch.bfloat16)
+    out = binding.gemv_w4(x.cuda(), codes.cuda(), scales.cuda(), 32, epilogue=SWIGLU)
+    for row in out:
+        _check_swiglu(row, gate, torch.full_like(gate, up).bfloat16())
