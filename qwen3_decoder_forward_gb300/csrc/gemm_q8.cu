@@ -1,6 +1,7 @@
 // GEMM on 8-bit rows on the 5th-generation tensor cores: out[M,N] = (xq xs)(wq ws)^T, e4m3
 // operands with one fp32 scale per row of x and per row of w, fp32 accumulation in tensor memory.
-// The scales do not depend on k, so the product of the codes is scaled once, in the epilogue.
+// The scales do not depend on k, so the product of the codes is scaled once, in the epilogue, by the row's
+// scale and then by the column's (RowScale).
 //
 // What each has to do: M N K products of codes and, once each, K (M + N) bytes of codes and the
 // outputs.  Many rows are bound by the tensor cores (and, past a hundred microseconds, by the power they
@@ -51,6 +52,8 @@ struct G8 {
     static constexpr int STAGES = BN >= 128 ? 6 : BN >= 64 ? 8 : 10;
     static constexpr int SMEM = STAGES * STAGE + 256 + 1024;  // ring + barriers + alignment
     static constexpr int PITCH = (BN + 4) * 4;  // bytes of a row of sums in shared memory, 4 banks past the last row's
+    static constexpr int SCALES = G8_BM * PITCH;   // the rows' scales, behind the sums
+    static_assert(SCALES + G8_BM * 8 <= STAGES * STAGE, "sums and scales exceed the ring");
     static constexpr uint32_t TMEM_COLS = 2 * BN < 32 ? 32 : 2 * BN;
 };
 
@@ -120,6 +123,20 @@ __device__ __forceinline__ float4 load_from(uint32_t addr) {  // shared memory o
     return v;
 }
 
+// A row's scale as s f, f a power of two and 1 for any usual row: outputs are ((sum s) w) f.  The codes' sum is 0 or
+// 2^-18 to 2^48, so that its product with s is a normal number, and that product times w leaves fp32 only where
+// the output does.  (The two scales' product formed first may be zero, or infinite and with a zero sum NaN.)
+struct RowScale {
+    float s, f;
+    RowScale() = default;
+    __device__ __forceinline__ explicit RowScale(float scale) {
+        const float m = fabsf(scale);
+        f = m > 0x1p78f ? 0x1p56f : m < 0x1p-104f && m > 0.0f ? 0x1p-44f : 1.0f;
+        s = scale * (m > 0x1p78f ? 0x1p-56f : m < 0x1p-104f ? 0x1p44f : 1.0f);
+    }
+    __device__ __forceinline__ float times(float sum, float w) const { return sum * s * w * f; }
+};
+
 // 16 columns of one output row: what they need besides the accumulator, and their store.
 template <int EPI>
 struct Out16 {
@@ -135,14 +152,15 @@ struct Out16 {
                 r[j] = *(reinterpret_cast<const float4 *>(static_cast<const float *>(out) + row * N + col) + j);
         }
     }
-    __device__ __forceinline__ void store(const uint32_t *v, float sx, size_t row, int col, int N, void *out) const {
+    __device__ __forceinline__ void store(const uint32_t *v, const RowScale &sx, size_t row, int col, int N,
+                                          void *out) const {
         float y[16];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            y[4 * j] = __uint_as_float(v[4 * j]) * (sx * w[j].x);
-            y[4 * j + 1] = __uint_as_float(v[4 * j + 1]) * (sx * w[j].y);
-            y[4 * j + 2] = __uint_as_float(v[4 * j + 2]) * (sx * w[j].z);
-            y[4 * j + 3] = __uint_as_float(v[4 * j + 3]) * (sx * w[j].w);
+            y[4 * j] = sx.times(__uint_as_float(v[4 * j]), w[j].x);
+            y[4 * j + 1] = sx.times(__uint_as_float(v[4 * j + 1]), w[j].y);
+            y[4 * j + 2] = sx.times(__uint_as_float(v[4 * j + 2]), w[j].z);
+            y[4 * j + 3] = sx.times(__uint_as_float(v[4 * j + 3]), w[j].w);
         }
         if (EPI == EPI_SWIGLU) {
             uint32_t o[4];
@@ -315,12 +333,13 @@ __global__ void __launch_bounds__(G8_THREADS, 1) k_gemm_q8(const __grid_constant
             const int m0 = (int)(t / tiles_n) * G8_BM, n0 = (int)(t % tiles_n) * BN;
             const int row = m0 + q * 32 + lane;
             const bool live = row < M;
-            const float sx = live ? xs[row] : 0.0f;
+            const RowScale sx(live ? xs[row] : 0.0f);
             if (SPLIT) {  // its sums into shared memory, over the ring that the MMAs are done with
                 const bool done = warp_poll(&tm_full[a], 0, limit);
                 if (!done) warp_wait(idle, 0, WAIT_LIMIT_DEFAULT);
                 tc_fence_after();
                 float4 *dst = reinterpret_cast<float4 *>(smem + (q * 32 + lane) * T::PITCH);
+                if (half == 0 && live) *reinterpret_cast<RowScale *>(smem + T::SCALES + (q * 32 + lane) * 8) = sx;
 #pragma unroll
                 for (int c = half; c < BN / 16; c += 2) {
                     uint32_t v[16];
@@ -378,7 +397,7 @@ __global__ void __launch_bounds__(G8_THREADS, 1) k_gemm_q8(const __grid_constant
                     if (j < S)
 #pragma unroll
                         for (int h = 0; h < W / 4; ++h) part[h][j] = load_from(in_cta(mine + h * 16, j));
-                const float sx = xs[m0 + r];
+                const RowScale sx = *reinterpret_cast<const RowScale *>(smem + T::SCALES + r * 8);
                 float y[W];
 #pragma unroll
                 for (int h = 0; h < W / 4; ++h) {
@@ -392,10 +411,10 @@ __global__ void __launch_bounds__(G8_THREADS, 1) k_gemm_q8(const __grid_constant
                             v.w += part[h][j].w;
                         }
                     const float4 w = __ldg(reinterpret_cast<const float4 *>(ws + col) + h);
-                    y[4 * h] = v.x * (sx * w.x);
-                    y[4 * h + 1] = v.y * (sx * w.y);
-                    y[4 * h + 2] = v.z * (sx * w.z);
-                    y[4 * h + 3] = v.w * (sx * w.w);
+                    y[4 * h] = sx.times(v.x, w.x);
+                    y[4 * h + 1] = sx.times(v.y, w.y);
+                    y[4 * h + 2] = sx.times(v.z, w.z);
+                    y[4 * h + 3] = sx.times(v.w, w.w);
                 }
                 if (EPI == EPI_SWIGLU) {
                     uint2 o;
@@ -641,7 +660,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
         for (long long t = first; t < tiles; t += step, ++local) {
             const uint32_t a = local & 1;
             const int y = (int)(t / tiles_n) * P8_BM + (int)rank * 128 + q * 32, n0 = (int)(t % tiles_n) * P8_BN + part * 64;
-            float sx = y + lane < M ? __ldg(xs + y + lane) : 0.0f;
+            RowScale sx(y + lane < M ? __ldg(xs + y + lane) : 0.0f);
             // 16 columns' scales, the first ones while the MMAs run; columns past N, a multiple of 16,
             // take others' and are not stored
             float4 w[4];
@@ -653,7 +672,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
             read_scales(n0);
             // a wait that gave up leaves NaN in this tile and in those after it (added to a residual, too)
             gave_up = gave_up || !warp_poll(&tm_full[a], (local >> 1) & 1, limit);
-            if (gave_up) sx = __uint_as_float(NAN_BITS);
+            if (gave_up) sx.s = __uint_as_float(NAN_BITS);
             tc_fence_after();
             const uint32_t t_row = tmem + a * P8_BN + part * 64 + ((uint32_t)(q * 32) << 16);
             // the tile's rows of 64 bytes: 16-byte piece u of row r at u ^ (r / 2) % 4 (64-byte swizzle)
@@ -682,12 +701,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
                 float2 v[8];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 s2 = make_float2(sx, sx);
-                    v[2 * j] = mul2(make_float2(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1])),
-                                    mul2(s2, make_float2(w[j].x, w[j].y)));
-                    v[2 * j + 1] = mul2(make_float2(__uint_as_float(x[4 * j + 2]), __uint_as_float(x[4 * j + 3])),
-                                        mul2(s2, make_float2(w[j].z, w[j].w)));
+                    const float2 s2 = make_float2(sx.s, sx.s);
+                    v[2 * j] = mul2(mul2(make_float2(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1])), s2),
+                                    make_float2(w[j].x, w[j].y));
+                    v[2 * j + 1] = mul2(mul2(make_float2(__uint_as_float(x[4 * j + 2]), __uint_as_float(x[4 * j + 3])), s2),
+                                        make_float2(w[j].z, w[j].w));
                 }
+                if (sx.f != 1.0f)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = mul2(v[j], make_float2(sx.f, sx.f));
                 if (c < 3) read_scales(col + 16);
                 if (EPI == EPI_SWIGLU) {  // 16 columns are one piece of the tile's rows
                     uint32_t o[4];

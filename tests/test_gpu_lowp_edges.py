@@ -72,3 +72,39 @@ def test_gemv_w4_swiglu_over_the_range_of_gates(N, K, up):
     out = binding.gemv_w4(x.cuda(), codes.cuda(), scales.cuda(), 32, epilogue=SWIGLU)
     for row in out:
         _check_swiglu(row, gate, torch.full_like(gate, up).bfloat16())
+
+
+@pytest.mark.parametrize("M,N,K", FORMS)
+@pytest.mark.parametrize("epi", [F32, RESID])
+def test_gemm_q8_scales_whose_product_leaves_fp32(M, N, K, epi):
+    """Rows and weights far from 1: what counts is that the output is in range, not the scales' product."""
+    g = torch.Generator().manual_seed(M)
+    xq = torch.randint(0x70, 0x7F, (M, K), generator=g, dtype=torch.uint8).view(E4M3).cuda()  # 128 to 448
+    wq = torch.randint(0x70, 0x7F, (N, K), generator=g, dtype=torch.uint8).view(E4M3).cuda()
+    rows = [1.7 * 2.0 ** -80, 1.3 * 2.0 ** 90, 1.9, 1.1 * 2.0 ** -61, 1.5 * 2.0 ** -120, 1.2 * 2.0 ** 118, 2.0 ** -149, 0.0]
+    cols = [1.1 * 2.0 ** -62, 1.9 * 2.0 ** -100, 1.3, 1.7 * 2.0 ** -80, 1.2 * 2.0 ** 40, 1.5 * 2.0 ** -20, 1.6 * 2.0 ** 100]
+    xs = torch.tensor(rows).repeat(M // 8 + 1)[:M].cuda()
+    ws = torch.tensor(cols).repeat(N // 7 + 1)[:N].cuda()
+    a, b = xq.double(), wq.double()
+    y = (a @ b.T) * xs.double()[:, None] * ws.double()[None, :]  # the terms are of one sign
+    base = torch.randn(M, N, generator=g).cuda() if epi == RESID else None
+    out = binding.gemm_q8(xq, xs, wq, ws, epilogue=epi, out=None if base is None else base.clone())
+    ref = y if base is None else base.double() + y
+    tol = (K / 16 + 10) * 2 ** -23 * y.abs() + 2 ** -23 * ref.abs() + 2.0 ** -148
+    most = torch.finfo(torch.float32).max
+    past = y.abs() > 1.01 * most  # none is nearer to it
+    assert not bool(((y.abs() > 0.99 * most) ^ past).any())
+    assert torch.equal(torch.isinf(out), past) and not bool(torch.isnan(out).any())
+    err = (out.double() - ref).abs()
+    assert bool((err <= tol)[~past].all()), f"error / tolerance {float((err / tol)[~past].max()):.3g}"
+
+
+@pytest.mark.parametrize("M,N,K", FORMS)
+def test_gemm_q8_a_zero_sum_stays_zero(M, N, K):
+    """Scales whose product is past fp32's largest number, on rows whose products cancel or are zero."""
+    xq, wq = torch.zeros(M, K), torch.zeros(N, K)
+    xq[:, :2] = 1
+    wq[:, 0], wq[:, 1] = 1, -1
+    out = binding.gemm_q8(xq.to(E4M3).cuda(), torch.full((M,), 2.0 ** 90, device="cuda"), wq.to(E4M3).cuda(),
+                          torch.full((N,), 2.0 ** 90, device="cuda"))
+    assert not out.any()
