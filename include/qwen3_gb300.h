@@ -533,8 +533,8 @@ int qwen3_op_quant_q8(const void *x_dev, int32_t x_dtype, int32_t M, int32_t K, 
  * as qwen3_op_quant_q8 defines them (the quotient from h * gain, in fp32: the row's common factor
  * cancels).  h_dev fp32 [M, C], updated in place; delta_dev [M, C] of delta_dtype, or NULL (h is
  * only read, delta_dtype unused); gain_dev fp32 [C]; q_dev e4m3 [M, C]; scale_dev fp32 [M].  A
- * row of zeros has scale 0 and codes 0; a row whose mean square is not finite in fp32, or that
- * meets a non-finite gain, has a NaN scale and NaN codes.  C a multiple of 16, at most 16384;
+ * row of zeros has scale 0 and codes 0; a row whose mean square or whose h * gain is not finite in fp32 has a
+ * NaN scale and NaN codes.  C a multiple of 16, at most 16384;
  * h_dev and delta_dev 32-byte aligned, gain_dev and q_dev 16-byte; eps finite, >= 0.  Errors: as above. */
 int qwen3_op_add_rmsnorm_q8(float *h_dev, const void *delta_dev, int32_t delta_dtype, int32_t M, int32_t C,
                             const float *gain_dev, float eps, void *q_dev, float *scale_dev, void *stream);

@@ -108,3 +108,32 @@ def test_gemm_q8_a_zero_sum_stays_zero(M, N, K):
     out = binding.gemm_q8(xq.to(E4M3).cuda(), torch.full((M,), 2.0 ** 90, device="cuda"), wq.to(E4M3).cuda(),
                           torch.full((N,), 2.0 ** 90, device="cuda"))
     assert not out.any()
+
+
+@pytest.mark.parametrize("M,C", [(5, 16), (3, 1024), (700, 1040), (310, 4112), (2, 16384)])
+@pytest.mark.parametrize("delta", [None, torch.bfloat16])
+@pytest.mark.parametrize("eps", [0.0, 1e-38])
+def test_add_rmsnorm_q8_rows_whose_squares_underflow(M, C, delta, eps):
+    """Without an eps that carries them, the mean squares of tiny rows are below fp32's numbers."""
+    g = torch.Generator().manual_seed(M + C)
+    size = 10.0 ** -torch.linspace(0, 37, M)[torch.randperm(M, generator=g)]
+    h = (torch.randn(M, C, generator=g) * size[:, None]).cuda()
+    d = None if delta is None else (torch.randn(M, C, generator=g) * size[:, None]).to(delta).cuda()
+    gain = (1 + 0.05 * torch.randn(C, generator=g)).cuda()
+    h[M // 2] = 0
+    if d is not None:
+        d[M // 2] = 0
+    want = h.clone() if d is None else h + d.float()
+    q, s = binding.add_rmsnorm_q8(h, gain, eps, delta=d)
+    assert torch.equal(h, want)
+    hd = want.double()
+    eps32 = float(torch.tensor(eps, dtype=torch.float32))
+    y = hd / torch.sqrt(hd.pow(2).mean(dim=1, keepdim=True) + eps32) * gain.double()
+    y[M // 2] = 0
+    top = y.abs().amax(dim=1)
+    assert bool(torch.isfinite(s).all())
+    # as for ordinary rows, and h * gain may be a subnormal number: C terms of 2^-149 against the row's top
+    lost = 2.0 ** -149 / (hd * gain.double()).abs().amax(dim=1).clamp(min=2.0 ** -149)
+    live = top > 0
+    assert float(((s.double() * 448 / top.where(live, torch.ones_like(top)) - 1).abs() - lost)[live].max()) <= 42 * 2 ** -24
+    assert float(s[M // 2]) == 0.0 and not q[M // 2].float().any()
