@@ -555,7 +555,8 @@ int qwen3_op_gemm_q8(const void *xq_dev, const float *xs_dev, int32_t M, int32_t
  *   zeros_dev NULL:  scale = bf16(max|w| / 7),      zero = 8;
  *   else:            scale = bf16((hi - lo) / 15),  zero = clamp(rint(-lo / scale), 0, 15);
  *   code = clamp(rint(w / scale) + zero, 0, 15).
- * A scale that rounds to zero divides as 1; a group holding an infinity or NaN has a NaN scale.
+ * hi - lo does not overflow: every finite group is quantised.  A scale that rounds to zero divides as 1; a
+ * group holding an infinity or NaN has a NaN scale.
  * codes_dev [N, K/2], scales_dev bf16 [N, K/group], zeros_dev uint8 [N, K/group] or NULL.  K a
  * multiple of group; w_dev 32-byte aligned, codes_dev 16-byte.  Errors: E_INVALID, E_CUDA. */
 int qwen3_op_quant_w4(const void *w_dev, int32_t N, int32_t K, int32_t group, void *codes_dev, void *scales_dev,

@@ -10,7 +10,7 @@
 // are ties between two codes -- common for bf16 rows, whose 448 y is exact -- round to even
 // as the definition says and do not depend on the error of 1 / m.  fp32 rows, whose 448 y rounds,
 // take their quotient as a sum of two floats, so that every code is the nearest (exact_quotient).
-// Bound by HBM: 3 to 11 bytes an element.  A row's warps hold it whole, 32 bytes a load, so that each
+// Bound by HBM: 3 to 13 bytes an element.  A row's warps hold it whole, 32 bytes a load, so that each
 // byte moves once: 23,460 rows of 1,024 with a bf16 addend (264 MB) in 45.0 us, 5.9 TB/s, where a
 // copy of as many bytes takes 41.5; 23,460 bf16 rows of 2,048 (144 MB) in 25.3 us.  With 16-byte
 // loads the first took 48.3.
@@ -422,9 +422,12 @@ __global__ void __launch_bounds__(256) k_quant_w4(const bf16 *__restrict__ w, lo
             c[j / 4] += (uint32_t)v1 << (8 * (j & 3) + 4);
         }
     } else {  // as the definition says, step by step
-        sb = __float2bfloat16(ZEROS ? range / 15.0f : range / 7.0f);
+        float step = ZEROS ? range / 15.0f : range / 7.0f;
+        if (ZEROS && range > 3.4e38f)  // finite ends whose distance is past fp32: at a sixteenth of its size
+            step = (__bfloat162float(m) * 0.0625f - least * 0.0625f) / 15.0f * 16.0f;
+        sb = __float2bfloat16(step);
         const float s = __bfloat162float(sb);
-        const bool bad = !(s <= 3.4e38f);  // not finite, or the range overflows
+        const bool bad = !(s <= 3.4e38f);  // a group that is not finite
         const float div = bad || !(s > 0.0f) ? 1.0f : s;
         if (ZEROS) z = bad ? 0.0f : fminf(fmaxf(rintf(-least / div), 0.0f), 15.0f);
 #pragma unroll

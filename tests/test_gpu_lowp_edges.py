@@ -137,3 +137,42 @@ def test_add_rmsnorm_q8_rows_whose_squares_underflow(M, C, delta, eps):
     live = top > 0
     assert float(((s.double() * 448 / top.where(live, torch.ones_like(top)) - 1).abs() - lost)[live].max()) <= 42 * 2 ** -24
     assert float(s[M // 2]) == 0.0 and not q[M // 2].float().any()
+
+
+def _w4_reference(w, group, zeros):
+    """The definition on the CPU: fp32 operations that IEEE rounds alike everywhere, the range of a group
+    taken at a sixteenth of its size where it is past fp32."""
+    N, K = w.shape
+    g = w.cpu().float().view(N, K // group, group)
+    lo, hi = g.amin(dim=2).clamp(max=0), g.amax(dim=2).clamp(min=0)
+    if zeros:
+        wide = torch.isinf(hi - lo)
+        s = ((hi - lo) / torch.full_like(hi, 15)).where(~wide, (hi / 16 - lo / 16) / torch.full_like(hi, 15) * 16)
+    else:
+        s = g.abs().amax(dim=2) / torch.full_like(hi, 7)
+    s = s.to(torch.bfloat16)
+    div = torch.where(s.float() > 0, s.float(), torch.ones(()))
+    z = torch.round(-lo / div).clamp(0, 15) if zeros else torch.full_like(div, 8)
+    code = (torch.round(g / div[:, :, None]) + z[:, :, None]).clamp(0, 15).view(N, K).to(torch.uint8)
+    return code, s, z.to(torch.uint8)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_quant_w4_groups_far_from_one(group, zeros):
+    """Groups of every size a bf16 number has, subnormal ones and ranges past fp32's largest among them."""
+    g = torch.Generator().manual_seed(group)
+    N, K = 300, 4 * group
+    power = torch.cat([torch.arange(-139, 129), torch.full((N - 268,), 128)]).double()
+    w = (torch.rand(N, K, generator=g, dtype=torch.float64) * 2 - 1) * (2.0 ** power)[:, None] * 0.996
+    w[:, 0], w[:, 1] = 0.99 * 2.0 ** power, -0.99 * 2.0 ** power
+    w[:, group:2 * group] = w[:, group:2 * group].abs()
+    w = w.to(torch.bfloat16)
+    assert bool(torch.isfinite(w).all())
+    codes, scales, zp = binding.quant_w4(w.cuda(), group, with_zeros=zeros)
+    code, s, z = _w4_reference(w, group, zeros)
+    c = codes.cpu()
+    assert torch.equal(scales.cpu(), s)
+    assert torch.equal(torch.stack([c & 15, c >> 4], dim=2).view(N, K), code)
+    if zeros:
+        assert torch.equal(zp.cpu(), z)
