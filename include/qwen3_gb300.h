@@ -550,6 +550,11 @@ int qwen3_op_add_rmsnorm_q8(float *h_dev, const void *delta_dev, int32_t delta_d
 int qwen3_op_gemm_q8(const void *xq_dev, const float *xs_dev, int32_t M, int32_t K, const void *wq_dev,
                      const float *ws_dev, int32_t N, int32_t epilogue, void *out_dev, void *stream);
 
+/* How qwen3_op_gemm_q8 runs a size on the current device: *tile_cols columns of the output to a tile (256: 256 rows
+ * by pairs of CTAs; 128, 64 or 32: 128 rows by single CTAs), *k_shares CTAs (1, 2, 4, 8) sharing a tile's K.  Host only.
+ * Errors: E_INVALID, E_CUDA. */
+int qwen3_op_gemm_q8_plan(int32_t M, int32_t K, int32_t N, int32_t *tile_cols, int32_t *k_shares);
+
 /* Weights in 4 bits, from w_dev bf16 [N, K].  Per group of `group` columns of a row, with lo and hi
  * its least and greatest weight (lo at most 0, hi at least 0), / and rint in fp32:
  *   zeros_dev NULL:  scale = bf16(max|w| / 7),      zero = 8;
@@ -572,6 +577,12 @@ int qwen3_op_quant_w4(const void *w_dev, int32_t N, int32_t K, int32_t group, vo
 int qwen3_op_gemv_w4(const void *x_dev, const float *xs_dev, int32_t M, int32_t K, const void *codes_dev,
                      const void *scales_dev, const void *zeros_dev, int32_t group, int32_t N, int32_t epilogue,
                      void *out_dev, void *stream);
+
+/* How qwen3_op_gemv_w4's first pass of rows runs a size on the current device: CTAs of *warps warps, *col_shares of which
+ * share the columns of 32 rows of W, in clusters of *cluster that share them further; a cluster goes through *rounds
+ * tiles at most.  with_zeros: zero points are given.  Host only.  Errors: E_INVALID, E_CUDA. */
+int qwen3_op_gemv_w4_plan(int32_t M, int32_t K, int32_t group, int32_t with_zeros, int32_t N, int32_t *warps,
+                          int32_t *col_shares, int32_t *cluster, int32_t *rounds);
 
 /* Releases the context and its graphs.  Does not free the arena or any caller memory. */
 void qwen3_free(qwen3_ctx *ctx);

@@ -131,6 +131,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "qwen3_op_attn_decode": (ctypes.c_int, [_P, i32, _P, pi32, _P, pi32, _P, _P, _P, _P, _P, i32, i32, i32, i32,
                                                 ctypes.c_float, i32, _P, _P, sz, _P]),
         "qwen3_op_set_wait_limit": (None, [ctypes.c_uint32]),
+        "qwen3_op_gemm_q8_plan": (ctypes.c_int, [i32, i32, i32, pi32, pi32]),
+        "qwen3_op_gemv_w4_plan": (ctypes.c_int, [i32, i32, i32, i32, i32, pi32, pi32, pi32, pi32]),
         "qwen3_op_quant_q8": (ctypes.c_int, [_P, i32, i32, i32, _P, _P, _P]),
         "qwen3_op_add_rmsnorm_q8": (ctypes.c_int, [_P, _P, i32, i32, i32, _P, ctypes.c_float, _P, _P, _P]),
         "qwen3_op_gemm_q8": (ctypes.c_int, [_P, _P, i32, i32, _P, _P, i32, i32, _P, _P]),
@@ -432,6 +434,13 @@ def qwen3_op_gemm_q8(xq_ptr: int, xs_ptr: int, M: int, K: int, wq_ptr: int, ws_p
     _check(load_library().qwen3_op_gemm_q8(xq_ptr, xs_ptr, M, K, wq_ptr, ws_ptr, N, epilogue, out_ptr, stream), None)
 
 
+def qwen3_op_gemm_q8_plan(M: int, K: int, N: int):
+    """(columns of a tile, CTAs sharing its K) of gemm_q8 at this size on the current device."""
+    out = [ctypes.c_int32() for _ in range(2)]
+    _check(load_library().qwen3_op_gemm_q8_plan(M, K, N, *map(ctypes.byref, out)), None)
+    return tuple(v.value for v in out)
+
+
 def qwen3_op_quant_w4(w_ptr: int, N: int, K: int, group: int, codes_ptr: int, scales_ptr: int,
                       zeros_ptr: Optional[int], stream: int = 0):
     _check(load_library().qwen3_op_quant_w4(w_ptr, N, K, group, codes_ptr, scales_ptr, zeros_ptr, stream), None)
@@ -441,6 +450,13 @@ def qwen3_op_gemv_w4(x_ptr: int, xs_ptr: Optional[int], M: int, K: int, codes_pt
                      zeros_ptr: Optional[int], group: int, N: int, epilogue: int, out_ptr: int, stream: int = 0):
     _check(load_library().qwen3_op_gemv_w4(x_ptr, xs_ptr, M, K, codes_ptr, scales_ptr, zeros_ptr, group, N, epilogue,
                                            out_ptr, stream), None)
+
+
+def qwen3_op_gemv_w4_plan(M: int, K: int, group: int, with_zeros: bool, N: int):
+    """(warps of a CTA, warps sharing a row's columns, CTAs of a cluster, rounds of tiles) of gemv_w4 at this size."""
+    out = [ctypes.c_int32() for _ in range(4)]
+    _check(load_library().qwen3_op_gemv_w4_plan(M, K, group, int(with_zeros), N, *map(ctypes.byref, out)), None)
+    return tuple(v.value for v in out)
 
 
 class _TensorCalls:

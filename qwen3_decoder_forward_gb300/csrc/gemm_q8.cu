@@ -800,44 +800,51 @@ cudaError_t run_single(const Launch &lc, const uint8_t *xq, const float *xs, int
 // Both sides, in us: 33 x 1024 x 2048 with the residual 5.1 whole, 4.7 in 4 shares of K; x 8192 12.0 and
 // 6.0 (8 shares); x 24576 30.9 and 9.2; 33 x 1024 x 1024 3.9 and 4.3.  600 x 6144 x 1024 17.9 in single
 // CTAs, 9.8 in pairs; 600 x 2048 x 2048 8.2 and 10.4.
-template <int EPI>
-cudaError_t choose_q8(const Launch &lc, const uint8_t *xq, const float *xs, int M, int K, const uint8_t *wq, const float *ws,
-                      int N, void *out) {
+Q8Plan choose_q8(int num_sms, int M, int K, int N) {
     const long long kb = (K + G8_BK - 1) / G8_BK, rows = q8_box_rows(M), live = M < 128 ? M : 128;
     auto up = [](long long a, long long b) { return (a + b - 1) / b; };
-    long long best = up(up(M, P8_BM) * up(N, P8_BN), lc.num_sms / 2) * kb * 555 + 7450;
-    int bn = 256, S = 1;
+    long long best = up(up(M, P8_BM) * up(N, P8_BN), num_sms / 2) * kb * 555 + 7450;
+    Q8Plan plan;
     for (int b = 32; b <= 128; b *= 2)
         for (int s = 1; s <= MAX_SPLIT && s <= kb; s *= 2) {
             const long long tiles = up(M, G8_BM) * up(N, b);
             // CTAs at once: the GPCs of 152 SMs hold 36 clusters of 4 and 15 of 8
-            const long long at_once = s == 8 ? lc.num_sms * 15 / 19 : s == 4 ? lc.num_sms * 18 / 19 : lc.num_sms;
+            const long long at_once = s == 8 ? num_sms * 15 / 19 : s == 4 ? num_sms * 18 / 19 : num_sms;
             if (s > 1 && tiles * s > at_once) break;
             const long long block = (rows + b) * 137 / 100, loop = up(kb, s) * (block > 300 ? block : 300);
             const long long tile = 160 + b * 103 / 10 + live * b * 29 / 100, n = up(tiles * s, at_once);
             const long long clocks = n * loop + (n + 1) * tile / 2 + (s > 1 ? 2000 : 0);
             if (clocks < best) {
                 best = clocks;
-                bn = b;
-                S = s;
+                plan.tile_cols = b;
+                plan.k_shares = s;
             }
         }
-    switch (bn) {
+    return plan;
+}
+
+template <int EPI>
+cudaError_t run_plan(const Launch &lc, const uint8_t *xq, const float *xs, int M, int K, const uint8_t *wq, const float *ws,
+                     int N, void *out) {
+    const Q8Plan plan = choose_q8(lc.num_sms, M, K, N);
+    switch (plan.tile_cols) {
         case 256: return run_pair<EPI>(lc, xq, xs, M, K, wq, ws, N, out);
-        case 128: return run_single<128, EPI>(lc, xq, xs, M, K, wq, ws, N, out, S);
-        case 64: return run_single<64, EPI>(lc, xq, xs, M, K, wq, ws, N, out, S);
-        default: return run_single<32, EPI>(lc, xq, xs, M, K, wq, ws, N, out, S);
+        case 128: return run_single<128, EPI>(lc, xq, xs, M, K, wq, ws, N, out, plan.k_shares);
+        case 64: return run_single<64, EPI>(lc, xq, xs, M, K, wq, ws, N, out, plan.k_shares);
+        default: return run_single<32, EPI>(lc, xq, xs, M, K, wq, ws, N, out, plan.k_shares);
     }
 }
 
 }  // namespace
 
+Q8Plan plan_gemm_q8(int num_sms, int M, int K, int N) { return choose_q8(num_sms, M, K, N); }
+
 cudaError_t launch_gemm_q8(const Launch &lc, const uint8_t *xq, const float *xs, int M, int K, const uint8_t *wq,
                            const float *ws, int N, int epi, void *out) {
     switch (epi) {
-        case EPI_F32: return choose_q8<EPI_F32>(lc, xq, xs, M, K, wq, ws, N, out);
-        case EPI_RESID_ADD: return choose_q8<EPI_RESID_ADD>(lc, xq, xs, M, K, wq, ws, N, out);
-        case EPI_SWIGLU: return choose_q8<EPI_SWIGLU>(lc, xq, xs, M, K, wq, ws, N, out);
+        case EPI_F32: return run_plan<EPI_F32>(lc, xq, xs, M, K, wq, ws, N, out);
+        case EPI_RESID_ADD: return run_plan<EPI_RESID_ADD>(lc, xq, xs, M, K, wq, ws, N, out);
+        case EPI_SWIGLU: return run_plan<EPI_SWIGLU>(lc, xq, xs, M, K, wq, ws, N, out);
     }
     return cudaErrorInvalidValue;
 }

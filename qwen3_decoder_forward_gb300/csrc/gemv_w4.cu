@@ -432,6 +432,7 @@ __global__ void __launch_bounds__(W4<ZEROS, G, MT>::MAX_WARPS * 32, 1)
             if (n < a.N) held = static_cast<const float *>(a.out)[(size_t)m * a.N + n];
         }
         // shares of the tile: [warp][row][x row]
+        __syncwarp();
         if (i > 0) {  // the last tile's shares have been read
             if (a.S > 1)
                 cluster_wait();
@@ -500,12 +501,6 @@ __global__ void __launch_bounds__(W4<ZEROS, G, MT>::MAX_WARPS * 32, 1)
 int x_stride(int kslice) { return kslice * 2 + 64; }
 int x_bytes(int m, int kslice) { return m * x_stride(kslice); }  // shared memory of m rows of x
 
-// How the work is cut: NW warps to a CTA, S CTAs to a cluster, WK column shares in a CTA.
-struct W4Plan {
-    int NW = 0, S = 0, WK = 0, kslice = 0, tile_rows = 0, clusters = 0;
-    float ns = 0.0f;
-};
-
 // The cheapest cut by an estimate: x staged once per CTA, then rounds of tiles, each bound by the
 // warps' issue rate or by latency, and closed by a join (none where a warp has its rows' whole sums).
 // The constants were fitted to all cuts of 23 sizes (1 to 32 rows, K 256 to 16,384, N 500 to
@@ -534,7 +529,7 @@ W4Plan plan_w4(int num_sms, int M, int K, int N, int mt, int max_warps, int fixe
                 p.tile_rows = W4_ROWS * (NW / p.WK);
                 const int tiles = (N + p.tile_rows - 1) / p.tile_rows;
                 p.clusters = tiles < slots ? tiles : slots;
-                const int rounds = (tiles + p.clusters - 1) / p.clusters;
+                p.rounds = (tiles + p.clusters - 1) / p.clusters;
                 const int resident = (p.clusters * S + num_sms - 1) / num_sms;  // CTAs of the busiest SM
                 const int warps = resident * NW;
                 const int mine = (slice + p.WK - 1) / p.WK;  // boxes of a warp and tile
@@ -542,7 +537,7 @@ W4Plan plan_w4(int num_sms, int M, int K, int N, int mt, int max_warps, int fixe
                 const float tile_ns = fmaxf((float)mine * warps * box_ns, 700.0f + 300.0f * mine);
                 const float join_ns = S > 1 ? 2550.0f : p.WK > 1 ? 255.0f + 49.0f * mt : 50.0f;
                 p.ns = 1360.0f + 17.0f * warps + (float)x_bytes(M, p.kslice) * resident / 70.0f +
-                       rounds * (tile_ns + join_ns + 20.0f * p.WK * S);
+                       p.rounds * (tile_ns + join_ns + 20.0f * p.WK * S);
                 if (!best.NW || p.ns < best.ns) best = p;
             }
         }
@@ -562,10 +557,27 @@ bool make_map_w4(CUtensorMap *map, const uint8_t *codes, int N, int K) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <bool ZEROS, int G, int MT>
+W4Plan plan_for(int num_sms, int M, int K, int N) {
+    using T = W4<ZEROS, G, MT>;
+    return plan_w4(num_sms, M, K, N, MT, T::MAX_WARPS, T::FIXED, T::PER_WARP);
+}
+template <bool ZEROS, int G>
+W4Plan plan_rows(int num_sms, int M, int K, int N) {
+    return M <= 8 ? plan_for<ZEROS, G, 1>(num_sms, M, K, N)
+                  : M <= 16 ? plan_for<ZEROS, G, 2>(num_sms, M, K, N) : plan_for<ZEROS, G, 4>(num_sms, M, K, N);
+}
+
+// Rows of x a launch: 32, fewer where a cluster of 8 CTAs cannot hold 32 of this length.
+int pass_rows(int K) {
+    const int slice = ((K + W4_BK - 1) / W4_BK + 7) / 8 * W4_BK;
+    return x_bytes(32, slice) <= 96 * 1024 ? 32 : x_bytes(16, slice) <= 96 * 1024 ? 16 : 8;
+}
+
 template <bool XQ, bool ZEROS, int G, int MT>
 cudaError_t run_w4(const Launch &lc, W4Args a, const uint8_t *codes) {
     using T = W4<ZEROS, G, MT>;
-    const W4Plan p = plan_w4(lc.num_sms, a.M, a.K, a.N, MT, T::MAX_WARPS, T::FIXED, T::PER_WARP);
+    const W4Plan p = plan_for<ZEROS, G, MT>(lc.num_sms, a.M, a.K, a.N);
     if (!p.NW) return cudaErrorInvalidValue;
     a.NW = p.NW;
     a.S = p.S;
@@ -603,11 +615,18 @@ cudaError_t run_group(const Launch &lc, const W4Args &a, const uint8_t *codes, i
 
 }  // namespace
 
+W4Plan plan_gemv_w4(int num_sms, int M, int K, int N, int group, bool zeros) {
+    const int m = M < pass_rows(K) ? M : pass_rows(K);
+    switch (group) {
+        case 32: return zeros ? plan_rows<true, 32>(num_sms, m, K, N) : plan_rows<false, 32>(num_sms, m, K, N);
+        case 64: return zeros ? plan_rows<true, 64>(num_sms, m, K, N) : plan_rows<false, 64>(num_sms, m, K, N);
+        default: return zeros ? plan_rows<true, 128>(num_sms, m, K, N) : plan_rows<false, 128>(num_sms, m, K, N);
+    }
+}
+
 cudaError_t launch_gemv_w4(const Launch &lc, const void *x, const float *xs, int M, int K, const uint8_t *codes,
                            const bf16 *scales, const uint8_t *zeros, int group, int N, int epi, void *out) {
-    // rows of x a launch: 32, fewer where a cluster of 8 CTAs cannot hold 32 of this length
-    const int slice = ((K + W4_BK - 1) / W4_BK + 7) / 8 * W4_BK;
-    const int pass = x_bytes(32, slice) <= 96 * 1024 ? 32 : x_bytes(16, slice) <= 96 * 1024 ? 16 : 8;
+    const int pass = pass_rows(K);
     for (int m0 = 0; m0 < M; m0 += pass) {
         W4Args a = {};
         a.M = M - m0 < pass ? M - m0 : pass;

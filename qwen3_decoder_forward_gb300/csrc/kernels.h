@@ -324,9 +324,22 @@ cudaError_t launch_quant_w4(const Launch &lc, const bf16 *w, int N, int K, int g
 cudaError_t launch_gemm_q8(const Launch &lc, const uint8_t *xq, const float *xs, int M, int K, const uint8_t *wq,
                            const float *ws, int N, int epi, void *out);
 
+// How it runs: tiles of 256 columns by pairs of CTAs, or of 128, 64 or 32 by single ones, K shared by k_shares CTAs.
+struct Q8Plan {
+    int tile_cols = 256, k_shares = 1;
+};
+Q8Plan plan_gemm_q8(int num_sms, int M, int K, int N);
+
 // --- gemv_w4.cu (decode on 4-bit weights) -------------------------------------------------
 // x bf16 [M, K] (xs null) or e4m3 [M, K] with row scales xs.
 cudaError_t launch_gemv_w4(const Launch &lc, const void *x, const float *xs, int M, int K, const uint8_t *codes,
                            const bf16 *scales, const uint8_t *zeros, int group, int N, int epi, void *out);
+// How its first pass of rows runs: S CTAs to a cluster sharing the columns, of NW warps as NW / WK tiles of 32 rows of W by
+// WK shares of the columns; each cluster goes through `rounds` tiles at most.
+struct W4Plan {
+    int NW = 0, S = 0, WK = 0, kslice = 0, tile_rows = 0, clusters = 0, rounds = 0;
+    float ns = 0.0f;  // the estimate that it has
+};
+W4Plan plan_gemv_w4(int num_sms, int M, int K, int N, int group, bool zeros);
 
 }  // namespace q3

@@ -105,12 +105,31 @@ int qwen3_op_add_rmsnorm_q8(float *h, const void *delta, int32_t delta_dtype, in
     });
 }
 
+static bool gemm_q8_size(int32_t M, int32_t K, int32_t N) {
+    return M >= 1 && M <= MAX_SIZE && N >= 16 && N <= MAX_SIZE && N % 16 == 0 && K >= 16 && K <= MAX_SIZE && K % 16 == 0;
+}
+
+int qwen3_op_gemm_q8_plan(int32_t M, int32_t K, int32_t N, int32_t *tile_cols, int32_t *k_shares) {
+    return guarded([&]() -> int {
+        const char *call = "qwen3_op_gemm_q8_plan";
+        if (!tile_cols || !k_shares) return fail(QWEN3_E_INVALID, call, "NULL argument");
+        if (!gemm_q8_size(M, K, N)) return fail(QWEN3_E_INVALID, call, "bad size (N and K multiples of 16)");
+        Launch lc;
+        const cudaError_t e = make_launch(nullptr, &lc);
+        if (e != cudaSuccess) return done(e, call);
+        const Q8Plan p = plan_gemm_q8(lc.num_sms, M, K, N);
+        *tile_cols = p.tile_cols;
+        *k_shares = p.k_shares;
+        return QWEN3_OK;
+    });
+}
+
 int qwen3_op_gemm_q8(const void *xq, const float *xs, int32_t M, int32_t K, const void *wq, const float *ws, int32_t N,
                      int32_t epi, void *out, void *stream) {
     return guarded([&]() -> int {
         const char *call = "qwen3_op_gemm_q8";
         if (!xq || !xs || !wq || !ws || !out) return fail(QWEN3_E_INVALID, call, "NULL argument");
-        if (M < 1 || M > MAX_SIZE || N < 16 || N > MAX_SIZE || N % 16 || K < 16 || K > MAX_SIZE || K % 16)
+        if (!gemm_q8_size(M, K, N))
             return fail(QWEN3_E_INVALID, call, "bad size (N and K multiples of 16)");
         if (epi < QWEN3_EPI_F32 || epi > QWEN3_EPI_SWIGLU) return fail(QWEN3_E_INVALID, call, "unknown epilogue");
         if (!aligned16(xq, wq, ws, out) || misaligned(xs, 4))
@@ -143,6 +162,29 @@ int qwen3_op_quant_w4(const void *w, int32_t N, int32_t K, int32_t group, void *
     });
 }
 
+static bool gemv_w4_size(int32_t M, int32_t K, int32_t group, int32_t N) {
+    return M >= 1 && M <= MAX_SIZE && N >= 1 && N <= MAX_SIZE && K >= group && K <= 65536 && K % group == 0;
+}
+
+int qwen3_op_gemv_w4_plan(int32_t M, int32_t K, int32_t group, int32_t with_zeros, int32_t N, int32_t *warps,
+                          int32_t *col_shares, int32_t *cluster, int32_t *rounds) {
+    return guarded([&]() -> int {
+        const char *call = "qwen3_op_gemv_w4_plan";
+        if (!warps || !col_shares || !cluster || !rounds) return fail(QWEN3_E_INVALID, call, "NULL argument");
+        if (group != 32 && group != 64 && group != 128) return fail(QWEN3_E_INVALID, call, "group must be 32, 64 or 128");
+        if (!gemv_w4_size(M, K, group, N)) return fail(QWEN3_E_INVALID, call, "bad size (K a multiple of group, at most 65536)");
+        Launch lc;
+        const cudaError_t e = make_launch(nullptr, &lc);
+        if (e != cudaSuccess) return done(e, call);
+        const W4Plan p = plan_gemv_w4(lc.num_sms, M, K, N, group, with_zeros != 0);
+        *warps = p.NW;
+        *col_shares = p.WK;
+        *cluster = p.S;
+        *rounds = p.rounds;
+        return QWEN3_OK;
+    });
+}
+
 int qwen3_op_gemv_w4(const void *x, const float *xs, int32_t M, int32_t K, const void *codes, const void *scales,
                      const void *zeros, int32_t group, int32_t N, int32_t epi, void *out, void *stream) {
     return guarded([&]() -> int {
@@ -150,8 +192,7 @@ int qwen3_op_gemv_w4(const void *x, const float *xs, int32_t M, int32_t K, const
         if (!x || !codes || !scales || !out) return fail(QWEN3_E_INVALID, call, "NULL argument");
         if (group != 32 && group != 64 && group != 128) return fail(QWEN3_E_INVALID, call, "group must be 32, 64 or 128");
         if (epi < QWEN3_EPI_F32 || epi > QWEN3_EPI_SWIGLU) return fail(QWEN3_E_INVALID, call, "unknown epilogue");
-        if (M < 1 || M > MAX_SIZE || N < 1 || N > MAX_SIZE || K < group || K > 65536 || K % group ||
-            (epi == QWEN3_EPI_SWIGLU && N % 2))
+        if (!gemv_w4_size(M, K, group, N) || (epi == QWEN3_EPI_SWIGLU && N % 2))
             return fail(QWEN3_E_INVALID, call, "bad size (K a multiple of group, at most 65536; N even with SwiGLU)");
         if (!aligned16(x, codes, out) || misaligned(xs, 4) || misaligned(scales, 4) || misaligned(zeros, 4))
             return fail(QWEN3_E_INVALID, call, "x, codes and out must be 16-byte aligned (xs, scales and zeros 4)");
