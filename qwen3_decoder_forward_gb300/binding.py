@@ -476,12 +476,20 @@ class _TensorCalls:
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self.stream = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
         self.device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        self.new = self._allocation(torch)
+
+    @staticmethod
+    def _allocation(torch):
+        """The short way to new memory if torch has it and it makes what is asked for, else the public one."""
         try:
-            from torch._C._dynamo.guards import _empty_strided_cuda
-        except ImportError:
-            def _empty_strided_cuda(size, stride, dtype):
-                return torch.empty_strided(size, stride, dtype=dtype, device="cuda")
-        self.new = _empty_strided_cuda
+            from torch._C._dynamo.guards import _empty_strided_cuda as short
+
+            t = short((2, 3), (3, 1), torch.bfloat16)
+            if t.is_cuda and t.shape == (2, 3) and t.stride() == (3, 1) and t.dtype is torch.bfloat16:
+                return short
+        except Exception:  # a private call of torch: it may be missing, or take and give something else
+            pass
+        return lambda size, stride, dtype: torch.empty_strided(size, stride, dtype=dtype, device="cuda")
 
 
 _tensor_calls = None

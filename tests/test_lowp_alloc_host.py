@@ -1,0 +1,31 @@
+"""The tensor calls' new memory: a private call of torch where it does what is expected, the public one otherwise."""
+
+import sys
+import types
+
+import pytest
+import torch
+
+from qwen3_decoder_forward_gb300 import binding
+
+
+def _raises(*_):
+    raise TypeError("another signature")
+
+
+def _wrong(size, stride, dtype):
+    return torch.empty_strided(size, stride, dtype=dtype)  # on the host
+
+
+@pytest.mark.parametrize("short", [None, _raises, _wrong, lambda *a: None])
+def test_another_form_of_the_private_call_is_not_used(short, monkeypatch):
+    guards = types.ModuleType("torch._C._dynamo.guards")
+    if short is not None:
+        guards._empty_strided_cuda = short
+    monkeypatch.setitem(sys.modules, "torch._C._dynamo.guards", guards)
+    asked = []
+    monkeypatch.setattr(torch, "empty_strided", lambda *a, **k: asked.append((a, k)))
+    new = binding._TensorCalls._allocation(torch)
+    asked.clear()
+    new((4, 8), (8, 1), torch.float32)
+    assert asked == [(((4, 8), (8, 1)), dict(dtype=torch.float32, device="cuda"))]
