@@ -477,6 +477,20 @@ class _TensorCalls:
         self.stream = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
         self.device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         self.new = self._allocation(torch)
+        self.recording, self.changed = torch.is_grad_enabled, self._version_count(torch)
+
+    @staticmethod
+    def _version_count(torch):
+        """Tells autograd that the tensors of a tuple were changed in place; as _allocation."""
+        try:
+            short, t = torch._C._increment_version, torch.empty(0)
+            before = t._version
+            short((t,))
+            if t._version == before + 1:
+                return short
+        except Exception:
+            pass
+        return lambda tensors: torch.autograd.graph.increment_version(tensors[0])
 
     @staticmethod
     def _allocation(torch):
@@ -506,8 +520,13 @@ def _refuse(call: str, want: str):
     raise Qwen3Error(QWEN3_E_INVALID, f"{call}: expected dense CUDA tensors on one device: {want}")
 
 
+def _refuse_recorded(call: str):
+    raise Qwen3Error(QWEN3_E_INVALID, f"{call}: writes a tensor that requires a gradient (the calls are not recorded)")
+
+
 # The calls below are a few microseconds of host time each and often the smallest kernels' cost, so
-# their checks are written out instead of shared.
+# their checks are written out instead of shared.  None is recorded by autograd: outputs carry no gradient, and a
+# tensor of the caller's that a call writes (h, out) may not require one unless gradients are off.
 
 def quant_q8(x):
     """Rows of x [M, K] (fp32 or bf16) in 8 bits (qwen3_op_quant_q8): (e4m3 codes [M, K], fp32
@@ -545,6 +564,9 @@ def add_rmsnorm_q8(h, gain, eps: float, delta=None):
         if ((dtype is not c.f32 and dtype is not c.bf16) or delta.get_device() != i or delta.shape != shape
                 or not delta.is_contiguous()):
             _refuse("add_rmsnorm_q8", "delta fp32 or bf16 [M, C], as h, or None")
+        if h.requires_grad and c.recording():
+            _refuse_recorded("add_rmsnorm_q8")
+        c.changed((h,))  # for autograd, which may have saved it
         ptr = delta.data_ptr()
         if dtype is c.bf16:
             dt = QWEN3_DT_BF16
@@ -568,6 +590,9 @@ def _projection_out(c, call: str, M: int, N: int, epilogue: int, out, index: int
         return c.new((M, N), (N, 1), dtype)
     if out.dtype is not dtype or out.shape != (M, N) or out.get_device() != index or not out.is_contiguous():
         _refuse(call, f"out {dtype} {[M, N]}")
+    if out.requires_grad and c.recording():
+        _refuse_recorded(call)
+    c.changed((out,))
     return out
 
 

@@ -176,3 +176,37 @@ def test_quant_w4_groups_far_from_one(group, zeros):
     assert torch.equal(torch.stack([c & 15, c >> 4], dim=2).view(N, K), code)
     if zeros:
         assert torch.equal(zp.cpu(), z)
+
+
+def test_tensors_written_in_place_are_marked_as_changed():
+    """A tensor that autograd has saved and a call writes: the backward pass refuses it, as after torch's own calls.
+    One that requires a gradient itself is refused at the call, and is left as it was."""
+    h, gain, d = torch.ones(4, 64, device="cuda"), torch.ones(64, device="cuda"), torch.ones(4, 64, device="cuda")
+    xq, xs = binding.quant_q8(h)
+    wq, ws = binding.quant_q8(torch.ones(32, 64, device="cuda"))
+    codes, scales, _ = binding.quant_w4(torch.ones(32, 64, device="cuda").bfloat16(), 32)
+    x, out = h.bfloat16(), torch.zeros(4, 32, device="cuda")
+    calls = {
+        "h": (h, lambda t: binding.add_rmsnorm_q8(t, gain, 1e-6, delta=d)),
+        "gemm out": (out, lambda t: binding.gemm_q8(xq, xs, wq, ws, epilogue=RESID, out=t)),
+        "gemv out": (out, lambda t: binding.gemv_w4(x, codes, scales, 32, out=t)),
+    }
+    for name, (t, call) in calls.items():
+        t = t.clone()
+        leaf = torch.ones_like(t, requires_grad=True)
+        y = (leaf * t).sum()  # saves t
+        call(t)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+        own = t.clone().requires_grad_()
+        before = own.detach().clone()
+        with pytest.raises(binding.Qwen3Error) as e:
+            call(own)
+        assert e.value.code == binding.QWEN3_E_INVALID and torch.equal(own.detach(), before), name
+        with torch.no_grad():
+            call(own)
+        with torch.inference_mode():
+            call(t.clone())
+    version = h._version  # without an addend h is only read
+    binding.add_rmsnorm_q8(h, gain, 1e-6)
+    assert h._version == version
