@@ -319,11 +319,11 @@ __global__ void __launch_bounds__(cta_warps(W) * 32) k_rows_q8_bf16(const bf16 *
 }
 
 // W warps to a row for rows of `warps` warps' worth: no more than hold it, so that a lane has its
-// four loads in flight, but up to 32 where there are few rows and the time is one row's latency (5 rows
-// of 1,024: 2.0 us with one load a lane, 3.0 with four).
+// four loads in flight, but up to 32 where there are few rows, two to an SM at most, and the time is one row's
+// latency (5 rows of 1,024: 2.0 us with one load a lane, 3.0 with four).
 template <typename Go>
-cudaError_t by_warps(int M, int warps, Go go) {
-    if (M <= 304) warps = warps * 4 < 32 ? warps * 4 : 32;
+cudaError_t by_warps(const Launch &lc, int M, int warps, Go go) {
+    if (M <= 2 * lc.num_sms) warps = warps * 4 < 32 ? warps * 4 : 32;
     if (warps <= 1) return go(std::integral_constant<int, 1>());
     if (warps <= 2) return go(std::integral_constant<int, 2>());
     if (warps <= 4) return go(std::integral_constant<int, 4>());
@@ -342,7 +342,7 @@ cudaError_t run_rows(const Launch &lc, const T *x, float *h, const float *gain, 
                      float *scale) {
     if constexpr (NORM && !TINY)
         if (eps < 0x1p-90f) return run_rows<T, NORM, HAS_D, true>(lc, x, h, gain, M, C, eps, q, scale);
-    return by_warps(M, (C + ROW_PER_WARP - 1) / ROW_PER_WARP, [&](auto w) {
+    return by_warps(lc, M, (C + ROW_PER_WARP - 1) / ROW_PER_WARP, [&](auto w) {
         constexpr int W = decltype(w)::value;
         return launch(lc, k_rows_q8<T, NORM, HAS_D, TINY, W>, row_grid(M, W), dim3(cta_warps(W) * 32), 0, x, h, gain, M, C, eps, q,
                       scale);
@@ -451,7 +451,7 @@ bool rows_q8_supported(int C) { return C >= 16 && C % 16 == 0 && C <= 16 * ROW_P
 
 cudaError_t launch_quant_q8(const Launch &lc, const void *x, bool x_bf16, int M, int K, uint8_t *q, float *scale) {
     if (x_bf16)
-        return by_warps(M, (K + BF_PER_WARP - 1) / BF_PER_WARP, [&](auto w) {
+        return by_warps(lc, M, (K + BF_PER_WARP - 1) / BF_PER_WARP, [&](auto w) {
             constexpr int W = decltype(w)::value;
             return launch(lc, k_rows_q8_bf16<W>, row_grid(M, W), dim3(cta_warps(W) * 32), 0, (const bf16 *)x, M, K, q, scale);
         });
