@@ -10,22 +10,25 @@
 // Two forms with the roles of the bf16 GEMM: one warp issues TMA loads of 128 k-bytes (128-byte
 // swizzle) into a ring, one issues tcgen05.mma kind::f8f6f4 into one of two accumulators, the others drain
 // the other accumulator.  The issuing warps run their loops whole and one elected lane issues: with one
-// lane alone in the loop, its operands went to uniform registers one at a time, and an MMA took 68 clocks
-// to issue, a commit 61, a k-block 530 whatever its tile -- more than the 512 of a pair's products.
-// Elected, an MMA takes 24 and a k-block 300 (23,460 x 6144 x 1024: 99.7 -> 86.7 us).
+// lane alone in the loop an MMA took 68 clocks to issue, a commit 61, a k-block 530 whatever its tile -- more
+// than the 512 of a pair's products.  Elected, an MMA takes 24 and a k-block 300 (23,460 x 6144 x 1024: 99.7 ->
+// 86.7 us).
 //   k_gemm_q8_pair: persistent over tiles of 256 x 256 by pairs of CTAs (cta_group::2).  Each CTA holds
 // 128 rows of x and 128 rows of w of a k-block, 32 KB, and the pair's tensor cores read both halves of w; a
 // 128 x 256 tile of one CTA would load 48 KB for the same products, more than the 64 bytes a clock
 // that an SM takes from L2 (such tiles ran at 2,770 TFLOP/s, what that rate allows).  Outputs
 // leave as TMA tiles of 32 rows: fp32 columns as they are, the residual as reducing stores
 // (each element is added to once, so the sum's bits do not depend on order; a subnormal sum may become
-// zero), SwiGLU pairs as bf16.  With SwiGLU 23,460 x 6144 x 1024 takes 86 us, 3,430 TFLOP/s; 8,191 x
-// 7,168 x 8,192 to fp32 282 us, 3,410 TFLOP/s, at the power limit (1,390 MHz when it runs on and on).
+// zero), SwiGLU pairs as bf16.  With SwiGLU 23,460 x 6144 x 1024 takes 86 us, 3,420 TFLOP/s, in bursts of some 40
+// launches, and 101 when it runs on and on; 8,191 x 7,168 x 8,192 to fp32 276 us, 3,490 TFLOP/s, and 319, at the power
+// limit (1,390 MHz).  23,460 x 1024 x 2048 with the residual, bound by bytes, 50.6 (floor 36.3).
 // Sharing the rows of x between two pairs by TMA multicast made mid sizes up to 8% faster and the
 // large ones up to 5% slower, and is not done.
 //   k_gemm_q8: tiles of 128 x BN by single CTAs, for few rows or few tiles: persistent, or, with fewer
 // tiles than SMs and a long K, a cluster of 2 to 8 CTAs to a tile, each with a share of K; the shares meet
-// in distributed shared memory in a fixed order.  33 x 1024 x 2048 with the residual: 3.9 us.
+// in distributed shared memory in a fixed order.  33 x 1024 x 2048 with the residual: 4.0 us; 128 x 4096 x 4096 6.8
+// (floor 2.9).  Between 200 and 4,096 rows both forms are 1.8 to 4.5 times their floor (2,048 x 6144 x 1024 11.9 us, 600
+// rows 7.2): a pair's first and last tile outside the products, rounds that are partly filled, rows stored by lanes.
 // M, N and K need not fill tiles: TMA zero-fills past the tensors' ends (a zero code adds
 // nothing) and drops what is stored past them; N and K are multiples of 16.
 // Every mbarrier wait is bounded.  A role that gives up stops; the epilogue then gives up too, and what it had not
@@ -490,7 +493,8 @@ __device__ __forceinline__ void commit_pair(uint64_t *bar) {
         : "memory");
 }
 // Arrives on a barrier of either CTA; relaxed, since what it orders is the accumulator's reads, which
-// tcgen05.wait::ld and the fence before it have completed (a release waits for this warp's stores).
+// tcgen05.wait::ld and the fence before it have completed (a release waits for this warp's stores): the PTX ISA's own
+// pattern between threads for tcgen05 (wait, fence::before_thread_sync, relaxed arrival; wait, fence::after_thread_sync).
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -793,7 +797,8 @@ cudaError_t run_single(const Launch &lc, const uint8_t *xq, const float *xs, int
 
 // The form, tile and split of K whose estimate is lowest.  In clocks past a launch's own, fitted to 1199
 // timed launches of 1 to 4,096 rows, K 512 to 24,576, N 272 to 8,192 (10% rms; what it picks is 0.8%
-// slower than the best of them on average, 23% at worst, where residuals of 200 rows bound it):
+// slower than the best of them on average, 23% at worst, where residuals of 200 rows bound it; not fitted again since
+// SwiGLU and the scales were changed):
 //   a k-block of a single CTA: 300 for its waits and issue, or 1.37 a row of its operands;
 //   a single CTA's tile: 160 + 10.3 a column + 0.29 an output, half hidden by the next tile's MMAs;
 //   joining a split tile: 2,000;  a k-block of a pair 555, its first and last tile 7,450.

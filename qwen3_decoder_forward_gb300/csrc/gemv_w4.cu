@@ -1,15 +1,18 @@
 // Decode projection on 4-bit weights: out[M,N] = x[M,K] . W[N,K]^T with W = s (code - z) per group of
-// G columns, for up to 32 rows of x a launch.  What it cannot do without is streaming the codes; what
-// bounds it is the issue of instructions: some 715 for a box of 8,192 codes and up to 8 rows of x, half of
-// them to make bf16 fragments of codes.  One row of a 151,936 x 1024 head takes 20 us (4.1 TB/s), 13 rows of
-// 8,192 x 10,240 21.7 us (2.0 TB/s), one of 4096 x 1024 a launch's 3.3 us.
+// G columns, for up to 32 rows of x a launch.  What it cannot do without is streaming the codes.  It does not reach
+// that: a box of 8,192 codes and up to 8 rows of x takes some 715 instructions, half of them to make bf16 fragments
+// of codes, and with few rows and 16 warps an SM their issue is near half of what bounds it (IPC 2.3); from 9 rows on,
+// with 8 warps an SM and 96 to 144 of 152 SMs in use, a warp waits on its own chain of conversion and mma.sync (13
+// rows: IPC 1.5, no pipe above 30%).  One row of a 151,936 x 1024 head takes 19.2 us (4.2 TB/s; floor 12.1), one of
+// 8,192 x 10,240 13.2 (6.5), 13 rows of it 21.8 (6.7), 32 of 16,384 x 4,096 28 (5.5), one of 4096 x 1024 a launch's 3.0.
 //
 // Sum over a row of W:  sum_groups s_g sum_{k in g} (code_k - z_g) x_k.  code - z is a small integer,
 // exact in bf16, so the inner sums run on the tensor cores (mma.sync m16n8k16, weight rows as the
 // M side, rows of x as the N side) and a group's sum is multiplied by its scale in fp32.
 //   A 32-bit word holds 8 codes of one row: (w >> 4i) & 0x000f000f | 0x43004300 is the bf16 pair
 // (128 + code_i, 128 + code_{i+4}), and one exact packed subtraction of 128 + z leaves the A
-// fragment.  x is staged once per CTA as bf16 (exact from e4m3) with every 8 columns in the
+// fragment (integers made floats by setting the exponent above their bits, as published for weights of few bits by
+// Kim, Henry, Fahim and Awadalla, "Who Says Elephants Can't Run", 2022).  x is staged once per CTA as bf16 (exact from e4m3) with every 8 columns in the
 // matching order (0,4,1,5,2,6,3,7), so the B fragments of two steps are one 16-byte read.
 //   A 32-row tile of W moves in boxes of 256 columns (128 bytes a row) by TMA into a ring of
 // the warp's own, swizzled so that the 32 lanes' 4-byte reads (8 rows x 4 words of one 16-byte piece)
@@ -504,7 +507,9 @@ int x_bytes(int m, int kslice) { return m * x_stride(kslice); }  // shared memor
 // The cheapest cut by an estimate: x staged once per CTA, then rounds of tiles, each bound by the
 // warps' issue rate or by latency, and closed by a join (none where a warp has its rows' whole sums).
 // The constants were fitted to all cuts of 23 sizes (1 to 32 rows, K 256 to 16,384, N 500 to
-// 151,936): its choice is 1% slower than the best cut on average and 7% at worst; 8 warps sharing
+// 151,936): its choice was 1% slower than the best cut on average and 7% at worst, before launches overlapped and
+// x was staged by whole warps; not fitted again since.  It is low where x's staging counts: 32 x 6144 x 1024 4.7 us
+// against 7.6, 32 x 16,384 x 4,096 21.4 against 28.  8 warps sharing
 // a 32-row tile's columns, without clusters, are up to 2.2 times slower (32 rows, 100,000 x 1,024:
 // 64 against 29 us; 1 row, 500 x 16,384: 13.3 against 6.9).
 W4Plan plan_w4(int num_sms, int M, int K, int N, int mt, int max_warps, int fixed, int per_warp) {
