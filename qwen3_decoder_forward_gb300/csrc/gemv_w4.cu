@@ -1,9 +1,9 @@
 // Decode projection on 4-bit weights: out[M,N] = x[M,K] . W[N,K]^T with W = s (code - z) per group of
-// G columns, for up to 32 rows of x a launch.  What it cannot do without is streaming the codes.  It does not reach
-// that: a box of 8,192 codes and up to 8 rows of x takes some 715 instructions, half of them to make bf16 fragments
-// of codes, and with few rows and 16 warps an SM their issue is near half of what bounds it (IPC 2.3); from 9 rows on,
-// with 8 warps an SM and 96 to 144 of 152 SMs in use, a warp waits on its own chain of conversion and mma.sync (13
-// rows: IPC 1.5, no pipe above 30%).  One row of a 151,936 x 1024 head takes 19.2 us (4.2 TB/s; floor 12.1), one of
+// G columns, for up to 32 rows of x a launch.  What it cannot do without is streaming the codes, and it does not
+// reach that.  A box of 8,192 codes and up to 8 rows of x takes some 715 instructions, half of them to make bf16
+// fragments of codes: with 16 warps an SM their issue takes 58% of the slots (2 rows of the head, IPC 2.3).  From 9 rows
+// on, with 8 warps an SM and 96 to 144 of 152 SMs in use, a warp waits on its own chain of conversion and mma.sync (13
+// rows: IPC 1.5, no pipe above 30%).  In us, with the floor: one row of a 151,936 x 1024 head 19.2 (12.1), one of
 // 8,192 x 10,240 13.2 (6.5), 13 rows of it 21.8 (6.7), 32 of 16,384 x 4,096 28 (5.5), one of 4096 x 1024 a launch's 3.0.
 //
 // Sum over a row of W:  sum_groups s_g sum_{k in g} (code_k - z_g) x_k.  code - z is a small integer,
@@ -12,8 +12,9 @@
 //   A 32-bit word holds 8 codes of one row: (w >> 4i) & 0x000f000f | 0x43004300 is the bf16 pair
 // (128 + code_i, 128 + code_{i+4}), and one exact packed subtraction of 128 + z leaves the A
 // fragment (integers made floats by setting the exponent above their bits, as published for weights of few bits by
-// Kim, Henry, Fahim and Awadalla, "Who Says Elephants Can't Run", 2022).  x is staged once per CTA as bf16 (exact from e4m3) with every 8 columns in the
-// matching order (0,4,1,5,2,6,3,7), so the B fragments of two steps are one 16-byte read.
+// Kim, Henry, Fahim and Awadalla, "Who Says Elephants Can't Run", 2022).  x is staged once per CTA as bf16 (exact from
+// e4m3) with every 8 columns in the matching order (0,4,1,5,2,6,3,7), so the B fragments of two steps are one
+// 16-byte read.
 //   A 32-row tile of W moves in boxes of 256 columns (128 bytes a row) by TMA into a ring of
 // the warp's own, swizzled so that the 32 lanes' 4-byte reads (8 rows x 4 words of one 16-byte piece)
 // touch 32 banks.
